@@ -1,7 +1,8 @@
 """Python binding of libmoe.so, the MI355X (gfx950) MoE-layer hot path.
 
 Argument marshalling only: every function here has the name of a C entry
-point declared in ``include/moe.h``, checks that the tensors it is given have
+point declared in ``include/moe.h`` (the layer) or ``include/moe_block.h`` (the
+operators around it, bound in ``block.py``), checks that the tensors it is given have
 the documented dtype, device and contiguity, and passes their device pointers
 and the current HIP stream through ctypes. All arithmetic runs in the HIP
 kernels; there is no CPU path. If the library has not been built, every call
@@ -180,6 +181,7 @@ def load():
         "moe_grouped_gemm_slots": (st, [_SP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP,
                                         _VP, ctypes.c_size_t, _VP]),
     }
+    sig.update(block.signatures())
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -235,7 +237,8 @@ def _ok(status, where):
 _HOST_ONLY = frozenset(("moe_status_str", "moe_check_shape", "moe_plan_layout",
                         "moe_workspace_bytes", "moe_router_workspace_bytes", "moe_capacity_rows",
                         "moe_pool_bytes", "moe_backward_workspace_bytes",
-                        "moe_replica_grad_bytes"))
+                        "moe_replica_grad_bytes", "moe_rmsnorm_backward_workspace_bytes",
+                        "moe_mx_workspace_bytes", "moe_grad_workspace_bytes"))
 
 
 class _Recorder:
@@ -294,6 +297,12 @@ def moe_plan_layout(shape: Shape) -> dict:
     out = PlanLayoutT()
     _ok(load().moe_plan_layout(ctypes.byref(shape), ctypes.byref(out)), "moe_plan_layout")
     return {n: getattr(out, n) for n, _ in out._fields_}
+
+
+def plan_layout_total(shape: Shape) -> int:
+    """int32 elements of the plan block."""
+    n = shape.E // shape.R if shape.R > 0 else 0
+    return shape.R * (7 * n + 5) + 1 + shape.E * (3 * shape.R + 1)
 
 
 def moe_plan_bytes(shape: Shape) -> int:
@@ -724,3 +733,9 @@ def moe_ffn_backward_replicas(shape, buf, plan, w_gate, w_up, w_down, dy, dbuf, 
         _ptr(dw_up, f32, "dw_up", n), _ptr(dw_down, f32, "dw_down", n),
         _ptr(rgrad, f32, "rgrad"), _nbytes(rgrad), _ptr(ws, torch.uint8, "ws"), ws.numel(),
         _stream(stream)), "moe_ffn_backward_replicas")
+
+
+from . import block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

@@ -1,0 +1,102 @@
+// mx.h -- 8-bit blocks on gfx950: 32 values of a row share a power-of-two
+// scale (byte e + 127), codes are e4m3. Also the workspace of the 8-bit
+// grouped GEMM and the launchers of the operators around the layer.
+#pragma once
+
+#include "common.h"
+#include "moe_block.h"
+
+namespace moe {
+
+constexpr int kMxBlock = 32;
+
+// Scale byte of a block whose largest magnitude is `top`: the smallest e >=
+// -127 with top <= 448 * 2^e = 1.75 * 2^(e + 8), as e + 127. With top =
+// m * 2^x, m in [1, 2), e is x - 8 where m <= 1.75, else x - 7: adding
+// 0x1fffff to the bits carries into the exponent exactly when the mantissa
+// field exceeds 0x600000 (m > 1.75). Infinities and NaN give 255.
+__device__ __forceinline__ uint32_t mx_scale_byte(float top)
+{
+    const uint32_t b = __float_as_uint(top) & 0x7fffffffu;
+    if (b >= 0x7f800000u) return 255u;
+    const int e = (int)((b + 0x1fffffu) >> 23) - 8;
+    return (uint32_t)(e > 0 ? e : 0);
+}
+
+// 2^-e of that byte, exact: bits of 2^(127 - byte). Bytes 0..253 occur with
+// finite blocks (at most 247); 255 gives NaN, which makes every code NaN.
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte)
+{
+    if (byte == 255u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float((254u - byte) << 23);
+}
+
+// Four e4m3 codes, first in the low byte. The quotients are at most 448 in
+// magnitude, so the conversion (to nearest even) never saturates.
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// |v| for a block maximum. fmaxf drops a NaN operand; a NaN becomes an
+// infinity here so that its block is still seen to hold one.
+__device__ __forceinline__ float mx_abs(float v)
+{
+    const float a = fabsf(v);
+    return a == a ? a : __uint_as_float(0x7f800000u);
+}
+
+// 8-bit GEMM geometry: a workgroup tile is at most 256 rows x 256 weight rows
+// (gate/up: 128 of each), K in stages of 128 bytes (four scale blocks).
+constexpr int kMxTileN = 256;
+constexpr int kMxStage = 128;
+
+struct MxWsLayout {
+    size_t sched, vrow, h, hs, total;
+};
+inline MxWsLayout mx_ws_layout(const moe_shape_t& s)
+{
+    const size_t N = (size_t)s.T * s.k, n1 = N > 0 ? N : 1;
+    MxWsLayout w;
+    size_t o = 0;
+    w.sched = o; o = align256(o + (size_t)(2 * (s.E + 1)) * 4);
+    w.vrow = o;  o = align256(o + n1 * 4);
+    w.h = o;     o = align256(o + n1 * s.F);
+    w.hs = o;    o = align256(o + n1 * (s.F / kMxBlock));
+    w.total = o;
+    return w;
+}
+
+// Workgroups of the norm's backward, each with its own fp32 sums of dweight.
+constexpr int kNormBwdGroups = 512;
+inline int norm_bwd_groups(const moe_shape_t& s)
+{
+    return s.T < kNormBwdGroups ? s.T : kNormBwdGroups;
+}
+
+}  // namespace moe
+
+hipError_t moe_launch_rmsnorm(const moe_shape_t& s, const void* x, const void* residual,
+                              const void* weight, float eps, void* s_out, void* y, void* q,
+                              void* scales, float* rstd, hipStream_t st);
+hipError_t moe_launch_rmsnorm_backward(const moe_shape_t& s, const void* s_in, const void* weight,
+                                       const float* rstd, const void* dy, const void* ds, void* dx,
+                                       float* dweight, float* part, hipStream_t st);
+hipError_t moe_launch_mx_quantize(int64_t rows, int64_t cols, int dtype, const void* x, void* q,
+                                  void* scales, hipStream_t st);
+hipError_t moe_launch_permute_mx(const moe_shape_t& s, const void* q, const void* scales,
+                                 const int32_t* ids, const int32_t* eidx, const int32_t* plan,
+                                 void* buf_q, void* buf_s, int32_t* dest_row, int32_t* row_src,
+                                 hipStream_t st);
+struct MoeMxWeights {
+    const uint8_t *gate, *gate_s, *up, *up_s, *down, *down_s;
+};
+hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const void* a_s,
+                                      const int32_t* plan, const MoeMxWeights& w, void* y,
+                                      char* ws, hipStream_t st);
+size_t moe_grad_ws_bytes(int n, const moe_grad_t* g);
+hipError_t moe_launch_grad_norm(int n, const moe_grad_t* g, float* norm, int32_t* err, double* part,
+                                hipStream_t st);
+hipError_t moe_launch_grad_clip(int n, const moe_grad_t* g, float max_norm, const float* norm,
+                                hipStream_t st);

@@ -19,6 +19,7 @@
 // time, faster than the runtime's own device-to-device copy (5.3 TB/s on
 // 1 GiB), and its HBM counter bytes equal the algorithmic bytes (1.01x).
 #include "common.h"
+#include "mx.h"
 
 namespace {
 
@@ -145,6 +146,48 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(int T, int k, int E, 
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (c0 + 64 * i < row_vecs) dst[c0 + 64 * i] = v[i];
+    }
+}
+
+// The 8-bit dispatch: as permute_kernel on rows of H code bytes; the
+// wavefront of a row's first chunk also moves its H / 32 scale bytes (whole
+// dwords: H % 128 == 0).
+__global__ __launch_bounds__(kThreads) void permute_mx_kernel(int T, int k, int E, int R, int row_vecs,
+                                                              int nchunks, int scale_words,
+                                                              const uint4* __restrict__ q,
+                                                              const uint32_t* __restrict__ scales,
+                                                              const int32_t* __restrict__ ids,
+                                                              const int32_t* __restrict__ eidx,
+                                                              const int32_t* __restrict__ plan,
+                                                              uint4* __restrict__ buf_q,
+                                                              uint32_t* __restrict__ buf_s,
+                                                              int32_t* __restrict__ dest_row,
+                                                              int32_t* __restrict__ row_src)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t wid = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    if (wid >= (int64_t)T * nchunks) return;
+    const int t = (int)(wid / nchunks), ch = (int)(wid % nchunks);
+    const int N = T * k;
+    const int c = ch * 64 + lane;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < row_vecs) v = q[(size_t)t * row_vecs + c];
+    uint32_t sw = 0;  // the row's first 64 scale words, one per lane
+    if (ch == 0 && lane < scale_words) sw = scales[(size_t)t * scale_words + lane];
+    const int d = resolve_dests(t, k, E, R, N, ids, eidx, plan);
+    if (lane < k && ch == 0) {
+        dest_row[t * k + lane] = d;
+        if (d >= 0) row_src[d] = t;
+    }
+    for (int j = 0; j < k; ++j) {
+        const int dj = __builtin_amdgcn_readlane(d, j);
+        if (dj < 0) continue;
+        if (c < row_vecs) buf_q[(size_t)dj * row_vecs + c] = v;
+        if (ch == 0) {
+            if (lane < scale_words) buf_s[(size_t)dj * scale_words + lane] = sw;
+            for (int i = 64 + lane; i < scale_words; i += 64)
+                buf_s[(size_t)dj * scale_words + i] = scales[(size_t)t * scale_words + i];
+        }
     }
 }
 
@@ -318,4 +361,21 @@ hipError_t moe_launch_combine(const moe_shape_t& s, const void* y, const int32_t
                               const float* w, const void* shared_y, void* out, hipStream_t st)
 {
     return moe_launch_combine_rows(s, (int64_t)s.T * s.k, y, dest_row, w, shared_y, out, st);
+}
+
+hipError_t moe_launch_permute_mx(const moe_shape_t& s, const void* q, const void* scales,
+                                 const int32_t* ids, const int32_t* eidx, const int32_t* plan,
+                                 void* buf_q, void* buf_s, int32_t* dest_row, int32_t* row_src,
+                                 hipStream_t st)
+{
+    if (s.T == 0) return hipSuccess;
+    const int row_vecs = s.H / 16, scale_words = s.H / (4 * moe::kMxBlock);
+    const int nchunks = (row_vecs + 63) / 64;
+    const int64_t waves = (int64_t)s.T * nchunks;
+    const int grid = (int)((waves + kThreads / 64 - 1) / (kThreads / 64));
+    permute_mx_kernel<<<grid, kThreads, 0, st>>>(
+        s.T, s.k, s.E, s.R, row_vecs, nchunks, scale_words, static_cast<const uint4*>(q),
+        static_cast<const uint32_t*>(scales), ids, eidx, plan, static_cast<uint4*>(buf_q),
+        static_cast<uint32_t*>(buf_s), dest_row, row_src);
+    return hipGetLastError();
 }

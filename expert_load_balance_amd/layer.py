@@ -9,9 +9,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_BF16, Shape, moe_combine, moe_count_plan, moe_gemm_down, moe_gemm_gateup,
-               moe_gemm_schedule, moe_grouped_gemm_slots, moe_grouped_gemm_train, moe_permute,
-               moe_plan, moe_plan_layout, moe_prefetch_replicas, moe_route, moe_workspace_bytes)
+from . import (MOE_BF16, MX_BLOCK, Shape, moe_combine, moe_count_plan, moe_gemm_down,
+               moe_gemm_gateup, moe_gemm_schedule, moe_grouped_gemm_mx, moe_grouped_gemm_slots,
+               moe_grouped_gemm_train, moe_mx_workspace_bytes, moe_permute, moe_permute_mx, moe_plan,
+               moe_plan_layout, moe_prefetch_replicas, moe_rmsnorm, moe_route, moe_router,
+               moe_router_workspace_bytes, moe_workspace_bytes)
 
 STAGES = ("route", "count_plan", "permute", "gemm_schedule", "gemm_gateup", "gemm_down",
           "shared", "combine")
@@ -133,3 +135,74 @@ class MoeLayerBuffers:
         moe_combine(s, self.y, self.dest_row, self.w, shared_y, self.out, st)
         mark("combine", 1)
         return self.out
+
+
+class MoeLayerMx:
+    """Buffers and call sequence of a serving step: norm (with the residual's
+    addition), router, and the experts in 8-bit blocks.
+
+    A shape whose dtype is MOE_BF16 with H and F multiples of 128. Weights are
+    (codes, scales) pairs as moe_mx_quantize makes them. The buffers belong to
+    one call at a time: calls that may overlap take an object each.
+    """
+
+    def __init__(self, shape: Shape, device="cuda"):
+        self.shape = shape
+        T, H, E, k, R = shape.T, shape.H, shape.E, shape.k, shape.R
+        N, i32, u8, f32 = T * k, torch.int32, torch.uint8, torch.float32
+        self.s = alloc((T, H), torch.bfloat16, device)
+        self.xn = alloc((T, H), torch.bfloat16, device)
+        self.xq = alloc((T, H), u8, device)
+        self.xs = alloc((T, H // MX_BLOCK), u8, device)
+        self.logits = alloc((T, E), f32, device)
+        self.ids = alloc((T, k), i32, device)
+        self.w = alloc((T, k), f32, device)
+        self.err = torch.zeros(1, dtype=i32, device=device)
+        self.counts = alloc((E,), i32, device)
+        self.offsets = alloc((E + 1,), i32, device)
+        self.eidx = alloc((N,), i32, device)
+        self.rank_load = alloc((R,), i32, device)
+        self.plan = alloc((moe_plan_layout(shape)["total"],), i32, device)
+        self.buf_q = alloc((N, H), u8, device)
+        self.buf_s = alloc((N, H // MX_BLOCK), u8, device)
+        self.dest_row = alloc((T, k), i32, device)
+        self.row_src = alloc((N,), i32, device)
+        self.y = alloc((N, H), torch.bfloat16, device)
+        self.out = alloc((T, H), torch.bfloat16, device)
+
+        def bytes_(n):
+            return torch.empty(max(n, 256), dtype=u8, device=device)
+
+        # the bf16 layer's workspace also holds partial tiles of its GEMM; the
+        # count needs only the head of it, but its size is one per shape
+        self.ws = bytes_(moe_workspace_bytes(shape))
+        self.router_ws = bytes_(moe_router_workspace_bytes(shape))
+        self.mx_ws = bytes_(moe_mx_workspace_bytes(shape))
+
+    def experts(self, xq, xs, ids, w, w_gate, w_up, w_down, shared_y=None, stream=None):
+        """Count + plan, dispatch, the 8-bit grouped GEMM and the combine, from
+        the 8-bit rows and the router's choice (ids, gate weights w) to
+        self.out."""
+        s, st = self.shape, stream if stream is not None else torch.cuda.current_stream()
+        moe_count_plan(s, ids, self.counts, self.offsets, self.eidx, self.rank_load, self.err,
+                       self.ws, self.plan, st)
+        moe_permute_mx(s, xq, xs, ids, self.eidx, self.plan, self.buf_q, self.buf_s, self.dest_row,
+                       self.row_src, st)
+        moe_grouped_gemm_mx(s, self.buf_q, self.buf_s, self.plan, w_gate, w_up, w_down, self.y,
+                            self.mx_ws, st)
+        moe_combine(s, self.y, self.dest_row, w, shared_y, self.out, st)
+        return self.out
+
+    def forward(self, x, residual, norm_weight, eps, w_router, bias, w_gate, w_up, w_down,
+                stream=None):
+        """One step: returns (out, s), the experts' sum and the residual stream
+        x + residual that it is to be added to (the next norm's residual)."""
+        st = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(st):
+            self.err.zero_()
+        moe_rmsnorm(self.shape, x, norm_weight, eps, residual=residual, s=self.s, y=self.xn,
+                    q=self.xq, scales=self.xs, stream=st)
+        moe_router(self.shape, self.xn, w_router, bias, self.logits, self.ids, self.w, self.err,
+                   self.router_ws, st)
+        self.experts(self.xq, self.xs, self.ids, self.w, w_gate, w_up, w_down, stream=st)
+        return self.out, self.s
