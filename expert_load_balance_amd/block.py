@@ -57,28 +57,59 @@ def signatures():
     }
 
 
-def _ptr(t, dtype, name, numel=None, nullable=False):
-    """The package's pointer check, and that the tensor is where the launch is."""
-    p = _moe._ptr(t, dtype, name, numel, nullable)
-    if t is not None:
+_types = None
+
+
+def _env():
+    """(function giving the current device, activation types by moe_dtype, code
+    types, scale types, float32, int32), looked up once: a call's own cost counts beside a decode step's kernels."""
+    global _types
+    if _types is None:
         import torch
 
-        here = torch.cuda.current_device()
-        if t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
-    return p
+        def device():
+            try:
+                return torch.cuda.current_device()
+            except (RuntimeError, AssertionError):
+                return -2  # no GPU: no tensor is there (host tensors are on -1)
+
+        u8 = torch.uint8
+        _types = (device, {_moe.MOE_F32: (torch.float32,), _moe.MOE_BF16: (torch.bfloat16,)},
+                  (u8, torch.float8_e4m3fn), (u8, torch.float8_e8m0fnu), (torch.float32,), (torch.int32,))
+    return _types
 
 
-def _codes():
-    import torch
+def _ptr(t, types, name, numel, here, nullable=False):
+    """The package's pointer check, and that the tensor is where the launch
+    is. The common case is one line; what fails it is told apart below."""
+    if t is None and nullable:
+        return None
+    try:
+        if (t.get_device() == here and t.is_contiguous() and t.numel() >= numel
+                and (types is None or t.dtype in types)):
+            return t.data_ptr() or None
+    except AttributeError:
+        pass
+    _moe._ptr(t, types, name, numel, nullable)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
 
-    return (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
+
+def _stream(stream, here):
+    """The current device's current stream, or the one given."""
+    if stream is None:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # a Stream object costs more than the rest of the call
+            return raw(here)
+    return _moe._stream(stream)
 
 
-def _mx(q, scales, name, n, nullable=False):
+def _mx(q, scales, name, n, here, nullable=False):
     """Pointers of codes and scales of n values."""
-    ct, stp = _codes()
-    return (_ptr(q, ct, name, n, nullable), _ptr(scales, stp, name + " scales", n // MX_BLOCK, nullable))
+    _, _, ct, stp, _, _ = _env()
+    return (_ptr(q, ct, name, n, here, nullable),
+            _ptr(scales, stp, name + " scales", n // MX_BLOCK, here, nullable))
 
 
 def _bytes(t):
@@ -89,15 +120,16 @@ def moe_rmsnorm(shape, x, weight, eps, residual=None, s=None, y=None, q=None, sc
                 stream=None):
     """s = x + residual; y and (q, scales) = s * rstd * weight. Outputs that are
     None are not computed; at least one is needed."""
-    import torch
-
-    act, n = _moe._act_dtype(shape), shape.T * shape.H
-    qp, sp = _mx(q, scales, "q", n, nullable=True)
-    args = (ctypes.byref(shape), _ptr(x, act, "x", n), _ptr(residual, act, "residual", n, nullable=True),
-            _ptr(weight, act, "weight", shape.H), float(eps), _ptr(s, act, "s", n, nullable=True),
-            _ptr(y, act, "y", n, nullable=True), qp, sp,
-            _ptr(rstd, torch.float32, "rstd", shape.T, nullable=True), _moe._stream(stream))
-    _moe._ok(_moe.load().moe_rmsnorm(*args), "moe_rmsnorm")
+    dev, acts, ct, stp, f32, _ = _env()
+    here, T, H = dev(), shape.T, shape.H
+    act, n = acts.get(shape.dtype), T * H
+    st = _moe.load().moe_rmsnorm(
+        ctypes.byref(shape), _ptr(x, act, "x", n, here), _ptr(residual, act, "residual", n, here, True),
+        _ptr(weight, act, "weight", H, here), eps, _ptr(s, act, "s", n, here, True),
+        _ptr(y, act, "y", n, here, True), _ptr(q, ct, "q", n, here, True),
+        _ptr(scales, stp, "q scales", n // MX_BLOCK, here, True),
+        _ptr(rstd, f32, "rstd", T, here, True), _stream(stream, here))
+    _moe._ok(st, "moe_rmsnorm")
 
 
 def moe_rmsnorm_backward_workspace_bytes(shape) -> int:
@@ -106,44 +138,42 @@ def moe_rmsnorm_backward_workspace_bytes(shape) -> int:
 
 def moe_rmsnorm_backward(shape, s, weight, rstd, dy, dx, dweight, ws, ds=None, stream=None):
     """dx (of x and of residual alike; may be dy or ds) and dweight (float32)."""
-    import torch
-
-    act, f32, n = _moe._act_dtype(shape), torch.float32, shape.T * shape.H
-    args = (ctypes.byref(shape), _ptr(s, act, "s", n), _ptr(weight, act, "weight", shape.H),
-            _ptr(rstd, f32, "rstd", shape.T), _ptr(dy, act, "dy", n),
-            _ptr(ds, act, "ds", n, nullable=True), _ptr(dx, act, "dx", n),
-            _ptr(dweight, f32, "dweight", shape.H), _ptr(ws, None, "ws"), _bytes(ws),
-            _moe._stream(stream))
-    _moe._ok(_moe.load().moe_rmsnorm_backward(*args), "moe_rmsnorm_backward")
+    dev, acts, _, _, f32, _ = _env()
+    here, T, H = dev(), shape.T, shape.H
+    act, n = acts.get(shape.dtype), T * H
+    st = _moe.load().moe_rmsnorm_backward(
+        ctypes.byref(shape), _ptr(s, act, "s", n, here), _ptr(weight, act, "weight", H, here),
+        _ptr(rstd, f32, "rstd", T, here), _ptr(dy, act, "dy", n, here), _ptr(ds, act, "ds", n, here, True),
+        _ptr(dx, act, "dx", n, here), _ptr(dweight, f32, "dweight", H, here), _ptr(ws, None, "ws", 0, here),
+        _bytes(ws), _stream(stream, here))
+    _moe._ok(st, "moe_rmsnorm_backward")
 
 
 def moe_mx_quantize(x, q, scales, stream=None):
     """x [..., cols] (bfloat16 or float32) in 8-bit blocks along its last dimension."""
-    import torch
-
+    dev, acts, ct, stp, _, _ = _env()
+    here = dev()
     if x.dim() < 1:
         raise ValueError("x needs a dimension to cut into blocks")
-    cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
-    xp = _ptr(x, (torch.bfloat16, torch.float32), "x")
-    qp, sp = _mx(q, scales, "q", x.numel())
-    dt = _moe.MOE_BF16 if x.dtype == torch.bfloat16 else _moe.MOE_F32
-    _moe._ok(_moe.load().moe_mx_quantize(rows, cols, dt, xp, qp, sp, _moe._stream(stream)),
-             "moe_mx_quantize")
+    n, cols = x.numel(), x.shape[-1]
+    bf = x.dtype in acts[_moe.MOE_BF16]
+    st = _moe.load().moe_mx_quantize(
+        n // cols if cols else 0, cols, _moe.MOE_BF16 if bf else _moe.MOE_F32,
+        _ptr(x, acts[_moe.MOE_BF16] + acts[_moe.MOE_F32], "x", 0, here), _ptr(q, ct, "q", n, here),
+        _ptr(scales, stp, "q scales", n // MX_BLOCK, here), _stream(stream, here))
+    _moe._ok(st, "moe_mx_quantize")
 
 
 def moe_permute_mx(shape, q, scales, ids, eidx, plan, buf_q, buf_scales, dest_row, row_src, stream=None):
     """moe_permute for 8-bit rows."""
-    import torch
-
-    i32, N = torch.int32, shape.N
-    total = _moe.plan_layout_total(shape)
-    qp, sp = _mx(q, scales, "q", shape.T * shape.H)
-    bq, bs = _mx(buf_q, buf_scales, "buf_q", N * shape.H)
-    args = (ctypes.byref(shape), qp, sp, _ptr(ids, i32, "ids", N), _ptr(eidx, i32, "eidx", N),
-            _ptr(plan, i32, "plan", total), bq, bs, _ptr(dest_row, i32, "dest_row", N),
-            _ptr(row_src, i32, "row_src", N), _moe._stream(stream))
-    _moe._ok(_moe.load().moe_permute_mx(*args), "moe_permute_mx")
+    dev, _, _, _, _, i32 = _env()
+    here, N, H = dev(), shape.N, shape.H
+    st = _moe.load().moe_permute_mx(
+        ctypes.byref(shape), *_mx(q, scales, "q", shape.T * H, here), _ptr(ids, i32, "ids", N, here),
+        _ptr(eidx, i32, "eidx", N, here), _ptr(plan, i32, "plan", _moe.plan_layout_total(shape), here),
+        *_mx(buf_q, buf_scales, "buf_q", N * H, here), _ptr(dest_row, i32, "dest_row", N, here),
+        _ptr(row_src, i32, "row_src", N, here), _stream(stream, here))
+    _moe._ok(st, "moe_permute_mx")
 
 
 def moe_mx_workspace_bytes(shape) -> int:
@@ -153,32 +183,50 @@ def moe_mx_workspace_bytes(shape) -> int:
 def moe_grouped_gemm_mx(shape, a, a_scales, plan, w_gate, w_up, w_down, y, ws, stream=None):
     """moe_grouped_gemm on 8-bit blocks. w_gate, w_up, w_down: (codes, scales)
     of [E][F][H], [E][F][H] and [E][H][F]; y bfloat16 [N][H]."""
-    import torch
+    dev, acts, _, _, _, i32 = _env()
+    here, N, H = dev(), shape.N, shape.H
+    n = shape.E * shape.F * H
+    st = _moe.load().moe_grouped_gemm_mx(
+        ctypes.byref(shape), *_mx(a, a_scales, "a", N * H, here),
+        _ptr(plan, i32, "plan", _moe.plan_layout_total(shape), here), *_mx(*w_gate, "w_gate", n, here),
+        *_mx(*w_up, "w_up", n, here), *_mx(*w_down, "w_down", n, here),
+        _ptr(y, acts[_moe.MOE_BF16], "y", N * H, here), _ptr(ws, None, "ws", 0, here), _bytes(ws),
+        _stream(stream, here))
+    _moe._ok(st, "moe_grouped_gemm_mx")
 
-    n = shape.E * shape.F * shape.H
-    total = _moe.plan_layout_total(shape)
-    ap, asp = _mx(a, a_scales, "a", shape.N * shape.H)
-    args = (ctypes.byref(shape), ap, asp, _ptr(plan, torch.int32, "plan", total),
-            *_mx(*w_gate, "w_gate", n), *_mx(*w_up, "w_up", n), *_mx(*w_down, "w_down", n),
-            _ptr(y, torch.bfloat16, "y", shape.N * shape.H), _ptr(ws, None, "ws"), _bytes(ws),
-            _moe._stream(stream))
-    _moe._ok(_moe.load().moe_grouped_gemm_mx(*args), "moe_grouped_gemm_mx")
+
+def _columns(ts, other, here, what):
+    """(addresses, element counts, moe_dtypes) of a list of gradients. The
+    checks are the single pointer's, a column at a time: a step has hundreds of
+    tensors."""
+    _, acts, _, _, _, _ = _env()
+    f32, bf = acts[_moe.MOE_F32][0], acts[_moe.MOE_BF16][0]
+    try:
+        dts = [t.dtype for t in ts]
+        ok = (all([t.get_device() == here for t in ts]) and all([t.is_contiguous() for t in ts])
+              and all([d is f32 or d is bf for d in dts]))
+        if ok and other is not None:
+            ok = dts == [t.dtype for t in other] and [t.numel() for t in ts] == [t.numel() for t in other]
+    except AttributeError:
+        ok = False
+    if not ok:
+        for i, t in enumerate(ts):
+            _ptr(t, (f32, bf), f"{what} {i}", 0, here)
+            if other is not None and (t.dtype != other[i].dtype or t.numel() != other[i].numel()):
+                raise ValueError(f"{what} {i} differs from its gradient in type or size")
+    return ([t.data_ptr() for t in ts], [t.numel() for t in ts],
+            [_moe.MOE_BF16 if d is bf else _moe.MOE_F32 for d in dts])
 
 
-def _grad_list(grads, into=None):
-    import torch
-
-    if into is not None and len(into) != len(grads):
-        raise ValueError(f"{len(grads)} gradients and {len(into)} outputs")
-    arr = (GradT * max(len(grads), 1))()
-    types = (torch.float32, torch.bfloat16)
-    for i, g in enumerate(grads):
-        arr[i].src = _ptr(g, types, f"gradient {i}")
-        arr[i].count = g.numel()
-        arr[i].dtype = _moe.MOE_BF16 if g.dtype == torch.bfloat16 else _moe.MOE_F32
-        if into is not None:
-            arr[i].dst = _ptr(into[i], g.dtype, f"output {i}", g.numel())
-    return arr
+def _grad_list(grads, into, here):
+    """The moe_grad_t array of a list: four 64-bit words each (the last holds
+    the type and a zero)."""
+    n = len(grads)
+    src, count, dtype = _columns(grads, None, here, "gradient")
+    dst = src if into is None or into is grads else _columns(into, grads, here, "output")[0]
+    words = [0] * (4 * n)
+    words[0::4], words[1::4], words[2::4], words[3::4] = src, dst, count, dtype
+    return ctypes.cast((ctypes.c_uint64 * (4 * n))(*words), ctypes.POINTER(GradT)) if n else None
 
 
 def moe_grad_workspace_bytes(grads) -> int:
@@ -193,19 +241,21 @@ def moe_grad_norm(grads, norm, err, ws, stream=None):
     """norm (float32, one element) = the root of the sum of squares of all
     elements of a list of float32 and bfloat16 tensors; err (int32) gets
     ERR_NONFINITE when it is not finite."""
-    import torch
-
-    arr = _grad_list(grads)
-    args = (len(grads), arr, _ptr(norm, torch.float32, "norm", 1), _ptr(err, torch.int32, "err", 1),
-            _ptr(ws, None, "ws"), _bytes(ws), _moe._stream(stream))
-    _moe._ok(_moe.load().moe_grad_norm(*args), "moe_grad_norm")
+    dev, _, _, _, f32, i32 = _env()
+    here = dev()
+    st = _moe.load().moe_grad_norm(
+        len(grads), _grad_list(grads, None, here), _ptr(norm, f32, "norm", 1, here),
+        _ptr(err, i32, "err", 1, here), _ptr(ws, None, "ws", 0, here), _bytes(ws), _stream(stream, here))
+    _moe._ok(st, "moe_grad_norm")
 
 
 def moe_grad_clip(grads, into, max_norm, norm, stream=None):
     """into[i] = grads[i] * min(1, max_norm / norm); into may be grads."""
-    import torch
-
-    arr = _grad_list(grads, into)
-    args = (len(grads), arr, float(max_norm), _ptr(norm, torch.float32, "norm", 1),
-            _moe._stream(stream))
-    _moe._ok(_moe.load().moe_grad_clip(*args), "moe_grad_clip")
+    dev, _, _, _, f32, _ = _env()
+    here = dev()
+    if len(into) != len(grads):
+        raise ValueError(f"{len(grads)} gradients and {len(into)} outputs")
+    st = _moe.load().moe_grad_clip(
+        len(grads), _grad_list(grads, into, here), max_norm, _ptr(norm, f32, "norm", 1, here),
+        _stream(stream, here))
+    _moe._ok(st, "moe_grad_clip")

@@ -52,9 +52,10 @@ struct Vec<false> {
     }
 };
 
-// Sum over the workgroup; every thread gets it. red: 16 floats of LDS no
+// Sum over the workgroup; every thread gets it. red: 16 values of LDS no
 // other call of the same row uses.
-__device__ __forceinline__ float wg_sum(float v, float* red)
+template <typename T>
+__device__ __forceinline__ T wg_sum(T v, T* red)
 {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
@@ -62,9 +63,18 @@ __device__ __forceinline__ float wg_sum(float v, float* red)
     if (waves == 1) return v;
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
-    float t = 0.0f;
+    T t = 0;
     for (int i = 0; i < waves; ++i) t += red[i];
     return t;
+}
+
+// rstd from the sum of squares, in fp64 like the sum: rstd is then the
+// correctly rounded one but for a tie, and a code or a bf16 of v goes to the
+// other side of a rounding only by the two fp32 products. The memory traffic
+// hides the fp64 adds (one conversion and one multiply-add per element).
+__device__ __forceinline__ float rstd_of(double ss, int H, float eps)
+{
+    return (float)(1.0 / sqrt(ss / (double)H + (double)eps));
 }
 
 // s = round(x + residual) of one vector (the stored value is the normed one)
@@ -114,7 +124,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
                                                               uint8_t* scales, float* rstd)
 {
     using V = Vec<BF16>;
-    __shared__ float red[16];
+    __shared__ double red[16];
     const int64_t row = blockIdx.x, base = row * vecs;
     uint4 u[CH], r[CH], wv[CH];
 #pragma unroll
@@ -128,7 +138,8 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
             wv[i] = weight[c];
         }
     }
-    float f[CH][V::kN], ss = 0.0f;
+    float f[CH][V::kN];
+    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = i * blockDim.x + threadIdx.x;
@@ -136,9 +147,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
         else V::load(u[i], f[i]);
         if (s && c < vecs) s[base + c] = u[i];
 #pragma unroll
-        for (int k = 0; k < V::kN; ++k) ss = fmaf(f[i][k], f[i][k], ss);
+        for (int k = 0; k < V::kN; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
     }
-    const float rs = 1.0f / sqrtf(wg_sum(ss, red) / (float)H + eps);
+    const float rs = rstd_of(wg_sum(ss, red), H, eps);
     if (rstd && threadIdx.x == 0) rstd[row] = rs;
     if (!y && !q) return;
 #pragma unroll
@@ -162,9 +173,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_wide_kernel(int H, int ve
                                                                    uint8_t* q, uint8_t* scales, float* rstd)
 {
     using V = Vec<BF16>;
-    __shared__ float red[16];
+    __shared__ double red[16];
     const int64_t row = blockIdx.x, base = row * vecs;
-    float ss = 0.0f;
+    double ss = 0.0;
     for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
         float f[V::kN];
         uint4 u = x[base + c];
@@ -172,9 +183,9 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_wide_kernel(int H, int ve
         else V::load(u, f);
         if (s) s[base + c] = u;
 #pragma unroll
-        for (int k = 0; k < V::kN; ++k) ss = fmaf(f[k], f[k], ss);
+        for (int k = 0; k < V::kN; ++k) ss = fma((double)f[k], (double)f[k], ss);
     }
-    const float rs = 1.0f / sqrtf(wg_sum(ss, red) / (float)H + eps);
+    const float rs = rstd_of(wg_sum(ss, red), H, eps);
     if (rstd && threadIdx.x == 0) rstd[row] = rs;
     if (!y && !q) return;
     // s, where it is kept, may have replaced x or residual: read it back then
@@ -202,8 +213,8 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_wide_kernel(int H, int ve
 // Workgroup b takes rows b, b + G, ...; each thread keeps the fp32 sums of
 // its columns over those rows and writes them to part[b], so that the sum's
 // order is fixed.
-template <bool BF16, int CH>
-__global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_kernel(int T, int H, int vecs, const uint4* s,
+template <bool BF16, int CH, int TH>
+__global__ __launch_bounds__(TH) void rmsnorm_bwd_kernel(int T, int H, int vecs, const uint4* s,
                                                                   const uint4* __restrict__ weight,
                                                                   const float* __restrict__ rstd,
                                                                   const uint4* dy, const uint4* ds,
@@ -331,8 +342,17 @@ __global__ __launch_bounds__(1024) void dweight_kernel(int G, int H, const float
     const int col = threadIdx.x % kRedCols, grp = threadIdx.x / kRedCols;
     const int h = blockIdx.x * kRedCols + col;
     float a = 0.0f;
-    if (h < H)
-        for (int g = grp; g < G; g += 16) a += part[(int64_t)g * H + h];
+    if (h < H) {
+        int g = grp;
+        for (; g + 7 * 16 < G; g += 8 * 16) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)(g + 16 * i) * H + h];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a += v[i];
+        }
+        for (; g < G; g += 16) a += part[(int64_t)g * H + h];
+    }
     sh[grp][col] = a;
     __syncthreads();
     if (grp == 0 && h < H) {
@@ -398,27 +418,33 @@ hipError_t launch_norm(const moe_shape_t& sh, const void* x, const void* r, cons
     return hipGetLastError();
 }
 
+// The backward holds 7 vectors' worth of registers per vector of the row (s,
+// dy, ds, the weight and the fp32 sums), so it takes two vectors a thread on
+// up to 512 threads, then up to four.
 template <bool BF16>
 hipError_t launch_norm_bwd(const moe_shape_t& sh, const void* s, const void* w, const float* rstd,
                            const void* dy, const void* ds, void* dx, float* part, int G, hipStream_t st)
 {
     const int vecs = sh.H / Vec<BF16>::kN;
-    const RowSplit p = row_split(vecs);
     const uint4 *sv = static_cast<const uint4*>(s), *wv = static_cast<const uint4*>(w),
                 *dv = static_cast<const uint4*>(dy), *ev = static_cast<const uint4*>(ds);
     uint4* xv = static_cast<uint4*>(dx);
-    switch (p.ch) {
-#define MOE_NORM(C)                                                                                 \
-    case C:                                                                                         \
-        rmsnorm_bwd_kernel<BF16, C><<<G, p.threads, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev, xv, \
-                                                             part);                                 \
-        break;
-        MOE_NORM(1) MOE_NORM(2) MOE_NORM(3) MOE_NORM(4)
+    int t = 64;
+    while (t < 512 && vecs > 2 * t) t *= 2;
+    if (vecs > 4 * t) t = kMaxThreads;
+    const int ch = (vecs + t - 1) / t;
+#define MOE_NORM(C, TH)                                                                              \
+    rmsnorm_bwd_kernel<BF16, C, TH><<<G, t, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev, xv, part)
+    if (t <= 512 && ch == 1) MOE_NORM(1, 512);
+    else if (t <= 512 && ch == 2) MOE_NORM(2, 512);
+    else if (t <= 512 && ch == 3) MOE_NORM(3, 512);
+    else if (t <= 512) MOE_NORM(4, 512);
+    else if (ch == 3) MOE_NORM(3, kMaxThreads);
+    else if (ch == 4) MOE_NORM(4, kMaxThreads);
+    else
+        rmsnorm_bwd_wide_kernel<BF16><<<G, kMaxThreads, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev, xv,
+                                                                 part);
 #undef MOE_NORM
-    default:
-        rmsnorm_bwd_wide_kernel<BF16><<<G, p.threads, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev,
-                                                               xv, part);
-    }
     return hipGetLastError();
 }
 
