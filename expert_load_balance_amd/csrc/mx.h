@@ -47,23 +47,45 @@ __device__ __forceinline__ float mx_abs(float v)
     return a == a ? a : __uint_as_float(0x7f800000u);
 }
 
-// 8-bit GEMM geometry: a workgroup tile is at most 256 rows x 256 weight rows
-// (gate/up: 128 of each), K in stages of 128 bytes (four scale blocks).
+// 8-bit GEMM geometry: a workgroup tile is 256, 128, 64 or 32 rows (kinds 0..3)
+// x 256 weight rows (gate/up: 128 of each), K in stages of 128 bytes (four
+// scale blocks), on at most kGemmMaxGrid persistent workgroups.
 constexpr int kMxTileN = 256;
 constexpr int kMxStage = 128;
+constexpr int kMxKinds = 4;
+constexpr int kMxMinStages = 4;  // of a K-part
+__host__ __device__ constexpr int mx_rows(int kind) { return 256 >> kind; }
+
+// Upper bound on the K-parts of one kind in one launch: no more than the
+// workgroups, and than the tiles that N rows of E experts can make, cut into
+// parts of kMxMinStages.
+inline int64_t mx_part_units(const moe_shape_t& s, int kind)
+{
+    const int64_t N = (int64_t)s.T * s.k;
+    int64_t tiles = N / (kind == 0 ? 129 : kind == 3 ? 1 : mx_rows(kind + 1) + 1);
+    if (kind > 0 && tiles > s.E) tiles = s.E;  // at most one tail per expert
+    const int64_t gu = tiles * (s.F / (kMxTileN / 2)) * (s.H / kMxStage / kMxMinStages);
+    const int64_t dn = tiles * ((s.H + kMxTileN - 1) / kMxTileN) * (s.F / kMxStage / kMxMinStages);
+    const int64_t u = gu > dn ? gu : dn;
+    return u < kGemmMaxGrid ? u : kGemmMaxGrid;
+}
 
 struct MxWsLayout {
-    size_t sched, vrow, h, hs, total;
+    size_t sched, vrow, h, hs, part[kMxKinds], total;
 };
 inline MxWsLayout mx_ws_layout(const moe_shape_t& s)
 {
     const size_t N = (size_t)s.T * s.k, n1 = N > 0 ? N : 1;
     MxWsLayout w;
     size_t o = 0;
-    w.sched = o; o = align256(o + (size_t)(2 * (s.E + 1)) * 4);
+    w.sched = o; o = align256(o + (size_t)((kMxKinds + 1) * (s.E + 1)) * 4);
     w.vrow = o;  o = align256(o + n1 * 4);
     w.h = o;     o = align256(o + n1 * s.F);
     w.hs = o;    o = align256(o + n1 * (s.F / kMxBlock));
+    for (int k = 0; k < kMxKinds; ++k) {
+        w.part[k] = o;
+        o = align256(o + (size_t)mx_part_units(s, k) * mx_rows(k) * kMxTileN * 4);
+    }
     w.total = o;
     return w;
 }
