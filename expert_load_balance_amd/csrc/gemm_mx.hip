@@ -388,13 +388,16 @@ struct Geo {
     static constexpr int kA = kRows * kTK;
     static constexpr int kACopies = kRows / 32;              // per wave per stage
     static constexpr int kPerStage = kWCopies + kACopies + 2;
-    // LDS: slots of rows + weights, then their scales, then three row lists
-    static constexpr int kSlot = kA + kWBytes;
+    // LDS, kinds 1..3: slots of rows + weights, then their scales, then three
+    // row lists. Kind 0: two slots of rows, a ring of 22 weight units of 32
+    // rows (a stage takes 8), two slots of scales, the lists.
+    static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
     static constexpr int kScale = (kTN + kRows) * 4;
     static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > 4
                                                       ? 4 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
     static constexpr int kAhead = KIND == 0 ? 2 : kSlots - 1;  // stages copied ahead of the products
-    static constexpr int kScale0 = kSlots * kSlot;
+    static constexpr int kUnits = KIND == 0 ? 22 : 0, kUnit0 = kSlots * kSlot;
+    static constexpr int kScale0 = kUnit0 + kUnits * 4096;
     static constexpr int kList0 = kScale0 + kSlots * kScale;
     static constexpr int kBytes = kList0 + 3 * kRows * 4;
     // Stages of a unit in the stream: at least kAhead, so that the copies are
@@ -479,9 +482,9 @@ struct Copier {
     {
         copy16(buffer_of(ab, range()), aoff[i], st * kTK, slot + wave * 1024 + i * 4096);
     }
-    __device__ __forceinline__ void weight(int i, uint32_t slot, int wave) const
+    __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
-        copy16(buffer_of(i < 4 ? wb0 : wb1, range()), woff[i], st * kTK, slot + GE::kA + wave * 1024 + i * 4096);
+        copy16(buffer_of(i < 4 ? wb0 : wb1, range()), woff[i], st * kTK, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
@@ -491,7 +494,7 @@ struct Copier {
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
 #pragma unroll
-        for (int i = 0; i < kWCopies; ++i) weight(i, slot, wave);
+        for (int i = 0; i < kWCopies; ++i) weight(i, slot + GE::kA + i * 4096, wave);
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) row(i, slot, wave);
         scales(sslot, wave, lane);
@@ -722,9 +725,20 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 }
 
 // ------------------------------------------------------- 256-row tiles --
-// Bound by the matrix cores: two slots; a stage's fragments are all in
-// registers by its middle, where one barrier frees its slot for the copies of
-// the stage after next and shows that the next stage has landed.
+// A stage is 32 MFMAs of 64 cycles a wave on 66 KB of copies, and a CU's
+// copies run at about 55 GB/s (26 bytes a cycle), so the two are near each
+// other and have to overlap throughout. All copies of a stage in one of its
+// halves took 2.5 us a stage: the waves that issue them wait for the copy
+// path and their MFMAs with them. So each half issues its part:
+//   first half of stage s: the products of its first 64 values of K, the reads
+//     of the second 64, and the copies of weight units 0..5 of stage s + 2,
+//     into the six units of the ring that no stage in use holds;
+//   one barrier: stage s's fragments are all in registers (its units and its
+//     row slot are free) and stage s + 1 has landed (each wave waits for its
+//     own copies but the six it just issued);
+//   second half: the other products, the copies of units 6 and 7, of the rows
+//     and of the scales of stage s + 2, and the reads of stage s + 1's first
+//     64 values.
 template <int MODE>
 __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
 {
@@ -752,6 +766,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     Copier<MODE, 0> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0, odd = 0;  // this unit's number; parity of the stage being computed
+    constexpr int kEarly = GE::kUnits - 16;  // weight units copied in a stage's first half
     // the copies move on to the next unit
     auto follow = [&]() {
         if (cp.st == cp.KT) {
@@ -761,6 +776,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     };
     auto slot_u = [&](int n) { return lds_u + (uint32_t)n * GE::kSlot; };
     auto sslot_u = [&](int n) { return lds_u + GE::kScale0 + (uint32_t)n * GE::kScale; };
+    // ring units: first unit of the stage being computed, of the next, and of
+    // the one being copied
+    auto wrap = [&](int x) { return x >= GE::kUnits ? x - GE::kUnits : x; };
+    int wat = 0;
+    auto unit_u = [&](int first, int i) { return lds_u + GE::kUnit0 + (uint32_t)wrap(first + i) * 4096u; };
 
     i32x8 wf[2][4], tf[2][4];
     int ws[4], ts[4], wsn[4], tsn[4];  // scales of this stage and the next
@@ -768,16 +788,18 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     // lane's four chunks (half, half + 2, + 4, + 6) the others differ from
     // the first in address bits 5 and 6
     const uint32_t fc = (uint32_t)((half ^ swz(fr)) * 16);
-    const uint32_t wfa = (uint32_t)(GE::kA + (GE::wrow(wn, 0) + fr) * 128) + fc;
+    const uint32_t wfa = (uint32_t)(GE::kUnit0 + fr * 128) + fc;
     const uint32_t tfa = (uint32_t)((wm * 128 + fr) * 128) + fc;
     const uint32_t wsa = (uint32_t)(GE::kScale0 + (GE::wrow(wn, 0) + fr) * 4);
     const uint32_t tsa = (uint32_t)(GE::kScale0 + (kTN + wm * 128 + fr) * 4);
-    auto read = [&](int n, int kk, int id) {  // fragment id: 0..3 weights, 4..7 rows
-        const uint32_t at = ((id < 4 ? wfa : tfa) ^ (uint32_t)(64 * kk)) + (uint32_t)n * GE::kSlot;
+    // fragment id (0..3 weights, 4..7 rows) of the stage in row slot n whose
+    // weights start at unit w0 of the ring
+    auto read = [&](int n, int w0, int kk, int id) {
         if (id < 4) {
-            const int o = (GE::wrow(0, id) - GE::wrow(0, 0)) * 128;
-            wf[kk][id] = frag(lds + at + o, lds + (at ^ 32u) + o);
+            const uint32_t at = (wfa ^ (uint32_t)(64 * kk)) + (uint32_t)wrap(w0 + GE::wrow(wn, id) / 32) * 4096u;
+            wf[kk][id] = frag(lds + at, lds + (at ^ 32u));
         } else {
+            const uint32_t at = (tfa ^ (uint32_t)(64 * kk)) + (uint32_t)n * GE::kSlot;
             const int o = (id - 4) * 4096;
             tf[kk][id - 4] = frag(lds + at + o, lds + (at ^ 32u) + o);
         }
@@ -795,14 +817,20 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             ts[q] = (int)((uint32_t)tsn[q] >> (8 * half));
         }
     };
-    cp.stage(slot_u(0), sslot_u(0), wave, lane);
-    follow();
-    cp.stage(slot_u(1), sslot_u(1), wave, lane);
+    for (int n = 0; n < 2; ++n) {
+        follow();
+#pragma unroll
+        for (int i = 0; i < kWCopies; ++i) cp.weight(i, unit_u(8 * n, i), wave);
+#pragma unroll
+        for (int i = 0; i < GE::kACopies; ++i) cp.row(i, slot_u(n), wave);
+        cp.scales(sslot_u(n), wave, lane);
+        ++cp.st;
+    }
     wait_vm_lgkm<0>();
     slot_barrier();
 #pragma unroll
     for (int id = 0; id < 8; ++id) {
-        read(0, 0, id);
+        read(0, 0, 0, id);
         read_scale(0, id);
     }
     take_scales();
@@ -819,18 +847,12 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
         bool more2 = false;
         const int KT = GE::stream_stages(u.KT);
         for (int s = 0; s < KT; ++s) {
-            // first half: its products, and the reads of the second half
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3], ts[q >> 2]);
-                if (q < 8) read(odd, 1, q);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            wait_vm_lgkm<0>();
-            slot_barrier();  // the next stage has landed, and this one's slot is free
-            if (s == 0) {
+            // (no branch below this: the compiler would move the first half's
+            // products behind it, next to their uses)
+            if (s == 1) {
                 // the unit after next: its list goes to the place of the list
-                // of the unit before this one, whose epilogue is done
+                // of the unit before this one, whose epilogue every wave left
+                // before stage 0's barrier
                 more2 = j + 2 * g.P < end;
                 if (more2) {
                     u2 = unit_of<MODE, 0>(g, work, j + 2 * g.P);
@@ -838,22 +860,32 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
                 }
             }
             follow();
-            // second half: its products, the copies of the stage after next
-            // and the reads of the next stage's first half
+            const int wnext = wrap(wat + 8), wcopy = wrap(wnext + 8);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3], ts[q >> 2]);
+                if (q < 8) read(odd, wat, 1, q);
+                if ((q + 1) * kEarly / 16 > q * kEarly / 16)  // kEarly of them, evenly
+                    cp.weight(q * kEarly / 16, unit_u(wcopy, q * kEarly / 16), wave);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            wait_vm_lgkm<kEarly>();
+            slot_barrier();  // the next stage has landed, and this one's slots are free
             const uint32_t sl = slot_u(odd), ssl = sslot_u(odd);
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
                 acc[q >> 2][q & 3] = mfma<1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3], ts[q >> 2]);
-                if (q < 8) cp.weight(q, sl, wave);
-                else cp.row(q - 8, sl, wave);
+                if (q < kWCopies - kEarly) cp.weight(kEarly + q, unit_u(wcopy, kEarly + q), wave);
+                else if (q - (kWCopies - kEarly) < GE::kACopies) cp.row(q - (kWCopies - kEarly), sl, wave);
+                else if (q == kWCopies - kEarly + GE::kACopies) cp.scales(ssl, wave, lane);
                 if (q & 1) {
-                    read(odd ^ 1, 0, q >> 1);
+                    read(odd ^ 1, wnext, 0, q >> 1);
                     read_scale(odd ^ 1, q >> 1);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            cp.scales(ssl, wave, lane);
             ++cp.st;
+            wat = wnext;
             take_scales();
             odd ^= 1;
         }
