@@ -17,7 +17,8 @@
 // unscaled 8-bit instruction (half the rate) cuts the same way.
 //
 // Expert e's rows are its pieces in rank order (virtual rows), cut into
-// 256-row tiles and a tail of 32, 64, 128 or 256 (kinds 3..0): the matrix cores
+// 256-row tiles (128 where K is below 512 values) and a tail of 32, 64, 128
+// or 256 (kinds 3..0): the matrix cores
 // then work on little padding, and small groups, which only stream their
 // weights, keep more of the LDS for copies in flight. A persistent workgroup
 // of four waves per CU takes tiles of rows x 256 weight rows in the order
@@ -49,12 +50,13 @@ constexpr int kSplitRounds = 6;
 enum { kGateUp = 0, kDown = 1 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // schedule (int32): for each kind the prefix of the experts' tiles [E + 1],
 // then the prefix of their rows [E + 1]. Every workgroup computes it, the
 // first writes it, and workgroup b fills vrow[256 b ..], the buffer row of
 // each virtual row.
-__global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int N,
+__global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int N, int base,
                                                                const int32_t* __restrict__ plan,
                                                                int32_t* __restrict__ sched,
                                                                int32_t* __restrict__ vrow)
@@ -68,11 +70,13 @@ __global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int
         const int np = plan[L.piece_num + tid];
         for (int p = 0; p < np && p < R; ++p) c += plan[L.piece_cnt + (size_t)tid * R + p];
     }
-    const int tail = c % mx_rows(0);
-    sh[0][tid] = c / mx_rows(0) + (tail > mx_rows(1));
+    const int tail = c % mx_rows(base);
 #pragma unroll
-    for (int k = 1; k < kMxKinds; ++k)
-        sh[k][tid] = tail <= mx_rows(k) && tail > (k + 1 < kMxKinds ? mx_rows(k + 1) : 0);
+    for (int k = 0; k < kMxKinds; ++k) {
+        const int below = k + 1 < kMxKinds ? mx_rows(k + 1) : 0;
+        const bool last = tail > below && tail <= mx_rows(k);  // the tail's kind
+        sh[k][tid] = k < base ? 0 : (k == base ? c / mx_rows(base) : 0) + last;
+    }
     sh[kMxKinds][tid] = c;
     __syncthreads();
     for (int off = 1; off < kThreads; off <<= 1) {
@@ -156,16 +160,11 @@ __device__ __forceinline__ i32x8 frag(const char* p0, const char* p1)
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// acc += W T over one 64-value k-step: half KK (0, 1) of a 128-byte stage,
-// whose scale bytes sit in the words ws, ts (already shifted by 8 bits for
-// the upper lanes) at bytes 0 and 2.
-template <int KK>
-__device__ __forceinline__ f32x16 mfma(const i32x8& w, const i32x8& t, const f32x16& acc, int ws, int ts)
+// acc += W T over one 64-value k-step, with the scales in byte B of ws and ts.
+template <int B>
+__device__ __forceinline__ f32x16 mfma(const i32x8& w, const i32x8& t, const f32x16& acc, uint32_t ws, uint32_t ts)
 {
-    if constexpr (KK == 0)
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, 0, 0, 0, ws, 0, ts);
-    else
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, 0, 0, 2, ws, 2, ts);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, 0, 0, B, (int)ws, B, (int)ts);
 }
 
 // 16 codes to bf16, times their scale (the word's byte B as an exponent):
@@ -192,7 +191,6 @@ __device__ __forceinline__ Bf16x16 widen(const u32x4& c, uint32_t scales)
 // lane 32 down, b).
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
 {
-    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
     const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
     a = r[0];
     b = r[1];
@@ -285,19 +283,18 @@ __device__ __forceinline__ int opaque_v(int v)
 // ------------------------------------------------------------ work units --
 
 // Units of one kind: `full` whole tiles, then L leftover tiles in S K-parts
-// of KTp stages (S == 1: none). first: their place in the launch's numbering.
+// of at least kMxMinStages stages (S == 1: none). first: their place in the launch's numbering.
 struct KindWork {
-    int full, L, S, KTp, first, count;
+    int full, L, S, first, count;
 };
 __device__ __forceinline__ KindWork kind_work(int n, int first, int P, int KT)
 {
-    KindWork w{n, 0, 1, KT, first, n};
+    KindWork w{n, 0, 1, first, n};
     const int left = uni(n % P);
     if (left > 0 && n < kSplitRounds * P) {
         const int s0 = uni(min(P / left, KT / moe::kMxMinStages));
         if (s0 > 1) {
-            w.KTp = uni((KT + s0 - 1) / s0);
-            w.S = uni((KT + w.KTp - 1) / w.KTp);
+            w.S = s0;
             w.L = left;
             w.full = n - left;
             w.count = w.full + w.L * w.S;
@@ -312,7 +309,7 @@ struct Unit {
 };
 
 struct Gemm {
-    int E, ntn, H, F, P;
+    int E, ntn, H, F, P, base;  // base: kind of an expert's whole tiles
     const uint8_t *a, *as;
     const int32_t *sched, *vrow;
     const uint8_t *w0, *s0, *w1, *s1;
@@ -326,7 +323,7 @@ template <int MODE>
 __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 {
     const int KT = (MODE == kGateUp ? g.H : g.F) / kTK;
-    KindWork w{0, 0, 1, KT, 0, 0};
+    KindWork w{0, 0, 1, 0, 0};
     int first = 0;
     for (int k = 0; k <= kind; ++k) {
         w = kind_work(ldc(g.sched, k * (g.E + 1) + g.E) * g.ntn, first, g.P, KT);
@@ -351,7 +348,8 @@ __device__ __forceinline__ void tile_of(const Gemm& g, int t, Unit& u)
     const int first = ldc(ts, lo), mts = ldc(ts, lo + 1) - first;
     const int local = t - first * g.ntn;
     const int r0 = ldc(rs, lo), c = ldc(rs, lo + 1) - r0;
-    const int nt = local / mts, v0 = KIND == 0 ? local % mts * mx_rows(0) : c / mx_rows(0) * mx_rows(0);
+    const int nt = local / mts;
+    const int v0 = KIND == g.base ? local % mts * mx_rows(KIND) : c / mx_rows(g.base) * mx_rows(g.base);
     u.e = uni(lo);
     u.n0 = uni(nt * (MODE == kGateUp ? kTN / 2 : kTN));
     u.rows = uni(min(mx_rows(KIND), c - v0));
@@ -368,8 +366,9 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
     u.pidx = -1;
     if (t >= w.full) {  // parts of the leftover tiles, part-major
         u.pidx = uni(t - w.full);
-        u.k0 = uni(u.pidx / w.L * w.KTp);
-        u.KT = uni(min(u.KT - u.k0, w.KTp));
+        const int p = uni(u.pidx / w.L), KT = u.KT;
+        u.k0 = uni(p * KT / w.S);
+        u.KT = uni((p + 1) * KT / w.S) - u.k0;
         t = w.full + uni(u.pidx % w.L);
     }
     tile_of<MODE, KIND>(g, t, u);
@@ -389,16 +388,17 @@ struct Geo {
     static constexpr int kACopies = kRows / 32;              // per wave per stage
     static constexpr int kPerStage = kWCopies + kACopies + 2;
     // LDS, kinds 1..3: slots of rows + weights, then their scales, then three
-    // row lists. Kind 0: two slots of rows, a ring of 22 weight units of 32
-    // rows (a stage takes 8), two slots of scales, the lists.
+    // row lists. Kind 0: two slots of rows, a ring of 21 weight units of 32
+    // rows (a stage takes 8), the scales of up to four stages (16 bytes for
+    // each weight row, then for each row), the lists.
     static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
-    static constexpr int kScale = (kTN + kRows) * 4;
+    static constexpr int kScale = (kTN + kRows) * (KIND == 0 ? 16 : 4);
     static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > 4
                                                       ? 4 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
     static constexpr int kAhead = KIND == 0 ? 2 : kSlots - 1;  // stages copied ahead of the products
-    static constexpr int kUnits = KIND == 0 ? 22 : 0, kUnit0 = kSlots * kSlot;
+    static constexpr int kUnits = KIND == 0 ? 21 : 0, kUnit0 = kSlots * kSlot;
     static constexpr int kScale0 = kUnit0 + kUnits * 4096;
-    static constexpr int kList0 = kScale0 + kSlots * kScale;
+    static constexpr int kList0 = kScale0 + (KIND == 0 ? 1 : kSlots) * kScale;
     static constexpr int kBytes = kList0 + 3 * kRows * 4;
     // Stages of a unit in the stream: at least kAhead, so that the copies are
     // never more than one unit ahead.
@@ -700,7 +700,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                         const i32x8 tf = frag(p + c0, p + c1);
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            acc[b][q] = mfma<KK>(wf[q], tf, acc[b][q], (int)ws[q], (int)ts[b]);
+                            acc[b][q] = mfma<2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
                     }
                 };
                 kstep(std::integral_constant<int, 0>{});
@@ -731,14 +731,59 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 // halves took 2.5 us a stage: the waves that issue them wait for the copy
 // path and their MFMAs with them. So each half issues its part:
 //   first half of stage s: the products of its first 64 values of K, the reads
-//     of the second 64, and the copies of weight units 0..5 of stage s + 2,
-//     into the six units of the ring that no stage in use holds;
+//     of the second 64, and the copies of weight units 0..4 of stage s + 2,
+//     into the five units of the ring that no stage in use holds;
 //   one barrier: stage s's fragments are all in registers (its units and its
 //     row slot are free) and stage s + 1 has landed (each wave waits for its
-//     own copies but the six it just issued);
-//   second half: the other products, the copies of units 6 and 7, of the rows
-//     and of the scales of stage s + 2, and the reads of stage s + 1's first
-//     64 values.
+//     own copies but the five it just issued);
+//   second half: the other products, the copies of units 5..7 and of the rows
+//     of stage s + 2, and the reads of stage s + 1's first 64 values.
+// A copy of scales touches a line per lane and so takes the copy path as long
+// as a kilobyte of weights; 4 bytes a stage for each of the 512 rows cost 16 %
+// of the time. They come in groups of up to four stages instead (16 bytes a
+// row): a group waits in LDS, is read into registers in the last stage of the
+// group before it, and its place is filled again in the stage after.
+
+// Groups of scales of a workgroup's units of kind 0, in the order of the
+// stream: stages a .. a + len of K, loaded from stage a - skip on (the last 16
+// bytes of a row, near its end). No group but a whole unit has one stage.
+template <int MODE>
+struct ScaleStream {
+    const char *asb, *sb;
+    uint32_t asoff, wsoff;
+    int at, left, KT_all, len, skip;
+
+    __device__ __forceinline__ void setup(const Gemm& g, const Unit& u, const int32_t* list, int wave, int lane)
+    {
+        const int K = MODE == kGateUp ? g.H : g.F, KS = K / moe::kMxBlock, wrows = MODE == kGateUp ? g.F : g.H;
+        asb = uni_ptr((const char*)g.as + (MODE == kGateUp ? 0 : (size_t)u.x0 * KS));
+        sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + (size_t)u.e * wrows * KS);
+        at = u.k0;
+        left = Geo<MODE, 0>::stream_stages(u.KT);
+        KT_all = K / kTK;
+        const int r = 64 * wave + lane;
+        asoff = r < u.rows ? (MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r) * (uint32_t)KS : kZeroRow;
+        wsoff = (uint32_t)(MODE == kGateUp ? u.n0 + (r & 127) : min(u.n0 + r, wrows - 1)) * (uint32_t)KS;
+    }
+    __device__ __forceinline__ void nothing()  // the last unit's scales again, for no one
+    {
+        at = 0;
+        left = 0x7fffffff;
+    }
+    // copies the next group
+    __device__ __forceinline__ void copy(uint32_t lds, int wave)
+    {
+        const int from = min(at, KT_all - 4);
+        skip = at - from;
+        len = min(4 - skip, left);
+        if (left - len == 1 && len > 1) --len;
+        copy16(buffer_of(sb, kCopyRange), wsoff, from * 4, lds + wave * 1024);
+        copy16(buffer_of(asb, kCopyRange), asoff, from * 4, lds + kTN * 16 + wave * 1024);
+        at += len;
+        left -= len;
+    }
+};
+
 template <int MODE>
 __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
 {
@@ -775,7 +820,6 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
         }
     };
     auto slot_u = [&](int n) { return lds_u + (uint32_t)n * GE::kSlot; };
-    auto sslot_u = [&](int n) { return lds_u + GE::kScale0 + (uint32_t)n * GE::kScale; };
     // ring units: first unit of the stage being computed, of the next, and of
     // the one being copied
     auto wrap = [&](int x) { return x >= GE::kUnits ? x - GE::kUnits : x; };
@@ -783,15 +827,16 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     auto unit_u = [&](int first, int i) { return lds_u + GE::kUnit0 + (uint32_t)wrap(first + i) * 4096u; };
 
     i32x8 wf[2][4], tf[2][4];
-    int ws[4], ts[4], wsn[4], tsn[4];  // scales of this stage and the next
+    // Scales of this stage and the rest of its group: the lane's two bytes of
+    // each stage (blocks 0 and 2 of the four; 1 and 3 in the upper lanes),
+    // this stage's in the lowest.
+    u32x2 ws[4], ts[4];
     // fragment addresses: chunk c of row r is slot chunk c ^ swz(r); of a
     // lane's four chunks (half, half + 2, + 4, + 6) the others differ from
     // the first in address bits 5 and 6
     const uint32_t fc = (uint32_t)((half ^ swz(fr)) * 16);
     const uint32_t wfa = (uint32_t)(GE::kUnit0 + fr * 128) + fc;
     const uint32_t tfa = (uint32_t)((wm * 128 + fr) * 128) + fc;
-    const uint32_t wsa = (uint32_t)(GE::kScale0 + (GE::wrow(wn, 0) + fr) * 4);
-    const uint32_t tsa = (uint32_t)(GE::kScale0 + (kTN + wm * 128 + fr) * 4);
     // fragment id (0..3 weights, 4..7 rows) of the stage in row slot n whose
     // weights start at unit w0 of the ring
     auto read = [&](int n, int w0, int kk, int id) {
@@ -804,36 +849,72 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             tf[kk][id - 4] = frag(lds + at + o, lds + (at ^ 32u) + o);
         }
     };
-    auto read_scale = [&](int n, int id) {
-        const uint32_t so = (uint32_t)n * GE::kScale;
-        if (id < 4) wsn[id] = *reinterpret_cast<const int*>(lds + wsa + so + (GE::wrow(0, id) - GE::wrow(0, 0)) * 4);
-        else tsn[id - 4] = *reinterpret_cast<const int*>(lds + tsa + so + (id - 4) * 128);
+    // the group that waits in LDS
+    const uint32_t sel = half ? 0x07050301u : 0x06040200u;
+    auto pack = [&](const u32x4& v) {
+        return u32x2{__builtin_amdgcn_perm(v[1], v[0], sel), __builtin_amdgcn_perm(v[3], v[2], sel)};
     };
-    // this lane's blocks: bytes 0 and 2 of the word, 1 and 3 in the upper lanes
-    auto take_scales = [&]() {
+    auto read_group = [&](u32x2* w, u32x2* t, int skip) {
+        const char* p = lds + GE::kScale0;
+        u32x4 a[4], b[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            ws[q] = (int)((uint32_t)wsn[q] >> (8 * half));
-            ts[q] = (int)((uint32_t)tsn[q] >> (8 * half));
+            a[q] = *reinterpret_cast<const u32x4*>(p + (GE::wrow(wn, q) + fr) * 16);
+            b[q] = *reinterpret_cast<const u32x4*>(p + (kTN + wm * 128 + q * 32 + fr) * 16);
         }
+        __builtin_amdgcn_sched_barrier(0);  // all reads in flight together
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            w[q] = pack(a[q]);
+            t[q] = pack(b[q]);
+        }
+        if (skip > 0)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w[q] = __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, w[q]) >> (16 * skip));
+                t[q] = __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, t[q]) >> (16 * skip));
+            }
     };
+    // the next stage's scales: the next of the group, or the next group's
+    // first (selected: a branch here would be one below the products)
+    auto next_scale = [](u32x2& v, const u32x2& group, bool refill) {
+        const uint64_t next = __builtin_bit_cast(uint64_t, v) >> 16;
+        v = __builtin_bit_cast(u32x2, refill ? __builtin_bit_cast(uint64_t, group) : next);
+    };
+    // the scales' copies move on to the next unit and copy its next group
+    ScaleStream<MODE> sc;
+    auto copy_group = [&](int lists) {
+        if (sc.left == 0) {
+            if (more) sc.setup(g, un, list(lists + 1), wave, opaque_v(lane));
+            else sc.nothing();
+        }
+        sc.copy(lds_u + GE::kScale0, wave);
+    };
+    sc.setup(g, u, list(0), wave, lane);
+    sc.copy(lds_u + GE::kScale0, wave);
+    int glen = sc.len;         // stages of this group that are left
+    const int gskip = sc.skip;
     for (int n = 0; n < 2; ++n) {
         follow();
 #pragma unroll
         for (int i = 0; i < kWCopies; ++i) cp.weight(i, unit_u(8 * n, i), wave);
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) cp.row(i, slot_u(n), wave);
-        cp.scales(sslot_u(n), wave, lane);
         ++cp.st;
     }
     wait_vm_lgkm<0>();
     slot_barrier();
 #pragma unroll
-    for (int id = 0; id < 8; ++id) {
-        read(0, 0, 0, id);
-        read_scale(0, id);
-    }
-    take_scales();
+    for (int id = 0; id < 8; ++id) read(0, 0, 0, id);
+    read_group(ws, ts, gskip);
+    wait_vm_lgkm<0>();
+    slot_barrier();
+    copy_group(0);
+    int nlen = sc.len, nskip = sc.skip;  // the group in LDS
+    bool refill = false;                 // it has been read: its place is free
+    u32x2 wsn[4], tsn[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) wsn[q] = tsn[q] = u32x2{0, 0};
 
     for (;;) {
         f32x16 acc[4][4];
@@ -860,10 +941,19 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
                 }
             }
             follow();
+            if (refill) {  // read by every wave before the last barrier
+                copy_group(m);
+                nlen = sc.len;
+                nskip = sc.skip;
+            }
+            refill = glen == 1;
+            if (refill) {  // the next stage starts the group in LDS
+                read_group(wsn, tsn, nskip);
+            }
             const int wnext = wrap(wat + 8), wcopy = wrap(wnext + 8);
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-                acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3], ts[q >> 2]);
+                acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
                 if (q < 8) read(odd, wat, 1, q);
                 if ((q + 1) * kEarly / 16 > q * kEarly / 16)  // kEarly of them, evenly
                     cp.weight(q * kEarly / 16, unit_u(wcopy, q * kEarly / 16), wave);
@@ -871,23 +961,22 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             }
             wait_vm_lgkm<kEarly>();
             slot_barrier();  // the next stage has landed, and this one's slots are free
-            const uint32_t sl = slot_u(odd), ssl = sslot_u(odd);
+            const uint32_t sl = slot_u(odd);
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-                acc[q >> 2][q & 3] = mfma<1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3], ts[q >> 2]);
+                acc[q >> 2][q & 3] = mfma<1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
                 if (q < kWCopies - kEarly) cp.weight(kEarly + q, unit_u(wcopy, kEarly + q), wave);
                 else if (q - (kWCopies - kEarly) < GE::kACopies) cp.row(q - (kWCopies - kEarly), sl, wave);
-                else if (q == kWCopies - kEarly + GE::kACopies) cp.scales(ssl, wave, lane);
-                if (q & 1) {
-                    read(odd ^ 1, wnext, 0, q >> 1);
-                    read_scale(odd ^ 1, q >> 1);
-                }
+                if (q >= 2 && q < 10) read(odd ^ 1, wnext, 0, q - 2);
+                // scales that no product of this stage needs any more
+                if (q % 4 == 3) next_scale(ts[q >> 2], tsn[q >> 2], refill);
+                if (q >= 12) next_scale(ws[q - 12], wsn[q - 12], refill);
                 __builtin_amdgcn_sched_barrier(0);
             }
             ++cp.st;
             wat = wnext;
-            take_scales();
             odd ^= 1;
+            glen = refill ? nlen : glen - 1;
         }
         drain();
         if (u.pidx >= 0) {
@@ -997,7 +1086,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     const moe::MxWsLayout W = moe::mx_ws_layout(s);
     int32_t* sched = reinterpret_cast<int32_t*>(ws + W.sched);
     int32_t* vrow = reinterpret_cast<int32_t*>(ws + W.vrow);
-    mx_schedule_kernel<<<(N + kThreads - 1) / kThreads, kThreads, 0, st>>>(s.E, s.R, N, plan, sched, vrow);
+    mx_schedule_kernel<<<(N + kThreads - 1) / kThreads, kThreads, 0, st>>>(s.E, s.R, N, moe::mx_base(s), plan, sched, vrow);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     Gemm g;
@@ -1005,6 +1094,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.H = s.H;
     g.F = s.F;
     g.P = persistent_grid();
+    g.base = moe::mx_base(s);
     g.sched = sched;
     g.vrow = vrow;
     g.h = reinterpret_cast<uint8_t*>(ws + W.h);

@@ -56,14 +56,20 @@ constexpr int kMxKinds = 4;
 constexpr int kMxMinStages = 4;  // of a K-part
 __host__ __device__ constexpr int mx_rows(int kind) { return 256 >> kind; }
 
+// Kind of an expert's whole tiles: the 256-row kernel reads its scales 16
+// bytes (512 values of K) at a time.
+__host__ inline int mx_base(const moe_shape_t& s) { return s.H >= 512 && s.F >= 512 ? 0 : 1; }
+
 // Upper bound on the K-parts of one kind in one launch: no more than the
 // workgroups, and than the tiles that N rows of E experts can make, cut into
 // parts of kMxMinStages.
 inline int64_t mx_part_units(const moe_shape_t& s, int kind)
 {
     const int64_t N = (int64_t)s.T * s.k;
-    int64_t tiles = N / (kind == 0 ? 129 : kind == 3 ? 1 : mx_rows(kind + 1) + 1);
-    if (kind > 0 && tiles > s.E) tiles = s.E;  // at most one tail per expert
+    const int base = mx_base(s);
+    if (kind < base) return 0;
+    int64_t tiles = N / (kind + 1 == kMxKinds ? 1 : mx_rows(kind + 1) + 1);
+    if (kind > base && tiles > s.E) tiles = s.E;  // at most one tail per expert
     const int64_t gu = tiles * (s.F / (kMxTileN / 2)) * (s.H / kMxStage / kMxMinStages);
     const int64_t dn = tiles * ((s.H + kMxTileN - 1) / kMxTileN) * (s.F / kMxStage / kMxMinStages);
     const int64_t u = gu > dn ? gu : dn;

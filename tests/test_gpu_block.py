@@ -322,6 +322,9 @@ MX_CASES = [
     (400, 256, 40, 8, 128, 8, 0.6, None), (1000, 384, 7, 2, 256, 7, 2.0, None),
     (77, 1024, 256, 8, 128, 32, 0.2, None), (530, 128, 4, 2, 1152, 1, 0.0, [1, 2]),
     (5, 4096, 12, 4, 1536, 4, 0.0, None), (250, 2048, 12, 4, 768, 12, 0.1, None),
+    # 256-row tiles (H and F from 512 up), K of 4 to 9 stages, tails of each size
+    (300, 512, 1, 1, 640, 1, 0.0, None), (900, 640, 3, 2, 768, 3, 0.3, None), (1100, 896, 4, 1, 1152, 2, 0.1, None),
+    (530, 768, 2, 2, 512, 2, 0.0, None), (2100, 1152, 6, 2, 896, 3, 0.5, [0, 2, 3, 5]), (256, 1280, 1, 1, 512, 1, 0.0, None),
 ]
 
 
