@@ -70,12 +70,13 @@ __global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int
         const int np = plan[L.piece_num + tid];
         for (int p = 0; p < np && p < R; ++p) c += plan[L.piece_cnt + (size_t)tid * R + p];
     }
-    const int tail = c % mx_rows(base);
+    // an expert's rows are of one kind: whole tiles and a tail of kind `base`,
+    // or, where they fit a smaller tile, one of that kind
 #pragma unroll
     for (int k = 0; k < kMxKinds; ++k) {
         const int below = k + 1 < kMxKinds ? mx_rows(k + 1) : 0;
-        const bool last = tail > below && tail <= mx_rows(k);  // the tail's kind
-        sh[k][tid] = k < base ? 0 : (k == base ? c / mx_rows(base) : 0) + last;
+        const bool mine = k < base ? false : k == base ? c > below : c > below && c <= mx_rows(k);
+        sh[k][tid] = mine ? (c + mx_rows(k) - 1) / mx_rows(k) : 0;
     }
     sh[kMxKinds][tid] = c;
     __syncthreads();
@@ -333,7 +334,7 @@ __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 }
 
 // Tile t of the kind: its expert by the prefix of tiles, then N-tile, M-tile
-// (M fastest). A tail starts behind the expert's whole 256-row tiles.
+// (M fastest, so that an expert's tiles meet its weights in the L2 together).
 template <int MODE, int KIND>
 __device__ __forceinline__ void tile_of(const Gemm& g, int t, Unit& u)
 {
@@ -348,8 +349,7 @@ __device__ __forceinline__ void tile_of(const Gemm& g, int t, Unit& u)
     const int first = ldc(ts, lo), mts = ldc(ts, lo + 1) - first;
     const int local = t - first * g.ntn;
     const int r0 = ldc(rs, lo), c = ldc(rs, lo + 1) - r0;
-    const int nt = local / mts;
-    const int v0 = KIND == g.base ? local % mts * mx_rows(KIND) : c / mx_rows(g.base) * mx_rows(g.base);
+    const int nt = local / mts, v0 = local % mts * mx_rows(KIND);
     u.e = uni(lo);
     u.n0 = uni(nt * (MODE == kGateUp ? kTN / 2 : kTN));
     u.rows = uni(min(mx_rows(KIND), c - v0));
@@ -435,7 +435,9 @@ template <int MODE, int KIND>
 struct Copier {
     using GE = Geo<MODE, KIND>;
     const char *ab, *asb, *wb0, *wb1, *sb;
-    uint32_t aoff[GE::kACopies], woff[kWCopies], asoff, wsoff;
+    uint32_t aoff[GE::kACopies], woff, asoff, wsoff;
+    int rows32;        // bytes of 32 weight rows
+    bool upper;        // weight blocks 4..7 lie inside the matrix
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
 
     // list: the unit's row list in LDS (gate/up; down reads h in virtual order)
@@ -461,11 +463,12 @@ struct Copier {
             const int r = 8 * (wave + 4 * i) + (lane >> 3);
             aoff[i] = r < u.rows ? source(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16) : kZeroRow;
         }
-#pragma unroll
-        for (int i = 0; i < kWCopies; ++i) {
-            const int r = 8 * (wave + 4 * i) + (lane >> 3);
-            woff[i] = weight(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16);
-        }
+        // (blocks of 32 weight rows are 32 K bytes apart; in the down
+        // projection's last tile the upper four may lie past the matrix)
+        const int r0 = 8 * wave + (lane >> 3);
+        woff = (uint32_t)(u.n0 + r0) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r0)) * 16);
+        rows32 = 32 * K;
+        upper = MODE == kGateUp || u.n0 + kTN / 2 < wrows;
         const int ar = GE::kRows / 4 * wave + lane;
         asoff = lane < GE::kRows / 4 && ar < u.rows ? source(ar) * (uint32_t)KS : kZeroRow;
         wsoff = weight(64 * wave + lane) * (uint32_t)KS;
@@ -484,7 +487,8 @@ struct Copier {
     }
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
-        copy16(buffer_of(i < 4 ? wb0 : wb1, range()), woff[i], st * kTK, unit + wave * 1024);
+        copy16(buffer_of(i < 4 ? wb0 : wb1, i < 4 || upper ? range() : 0u), woff,
+               st * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
@@ -521,7 +525,7 @@ __device__ __forceinline__ void finish(const Gemm& g, const Unit& u, int i,
 {
     using GE = Geo<MODE, KIND>;
     const int fr = lane & 31, half = lane >> 5, wm = wave / GE::WN, wn = wave % GE::WN;
-    const int r = (wm * GE::TB + i) * 32 + fr;
+    const int r = (i * GE::WM + wm) * 32 + fr;
     const bool in = r < u.rows;
     if (MODE == kGateUp) {
         const int SF = g.F / moe::kMxBlock;
@@ -750,12 +754,15 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 template <int MODE>
 struct ScaleStream {
     const char *asb, *sb;
-    uint32_t asoff, wsoff;
-    int at, left, KT_all, len, skip;
+    uint32_t asoff;
+    int n0, wrows, KS, at, left, KT_all, len, skip;
 
     __device__ __forceinline__ void setup(const Gemm& g, const Unit& u, const int32_t* list, int wave, int lane)
     {
-        const int K = MODE == kGateUp ? g.H : g.F, KS = K / moe::kMxBlock, wrows = MODE == kGateUp ? g.F : g.H;
+        const int K = MODE == kGateUp ? g.H : g.F;
+        KS = K / moe::kMxBlock;
+        wrows = MODE == kGateUp ? g.F : g.H;
+        n0 = u.n0;
         asb = uni_ptr((const char*)g.as + (MODE == kGateUp ? 0 : (size_t)u.x0 * KS));
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + (size_t)u.e * wrows * KS);
         at = u.k0;
@@ -763,7 +770,6 @@ struct ScaleStream {
         KT_all = K / kTK;
         const int r = 64 * wave + lane;
         asoff = r < u.rows ? (MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r) * (uint32_t)KS : kZeroRow;
-        wsoff = (uint32_t)(MODE == kGateUp ? u.n0 + (r & 127) : min(u.n0 + r, wrows - 1)) * (uint32_t)KS;
     }
     __device__ __forceinline__ void nothing()  // the last unit's scales again, for no one
     {
@@ -771,8 +777,10 @@ struct ScaleStream {
         left = 0x7fffffff;
     }
     // copies the next group
-    __device__ __forceinline__ void copy(uint32_t lds, int wave)
+    __device__ __forceinline__ void copy(uint32_t lds, int wave, int lane)
     {
+        const int r = 64 * wave + lane;
+        const uint32_t wsoff = (uint32_t)(MODE == kGateUp ? n0 + (r & 127) : min(n0 + r, wrows - 1)) * (uint32_t)KS;
         const int from = min(at, KT_all - 4);
         skip = at - from;
         len = min(4 - skip, left);
@@ -790,7 +798,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     using GE = Geo<MODE, 0>;
     const KindWork work = work_of<MODE>(g, 0);
     const int end = work.count;
-    int j = slot_id;
+    // Round r's tile at position p goes to slot p + r: tails lie between whole
+    // tiles at regular distances, and no slot should get only the one or the
+    // other.
+    auto unit_at = [&](int r) { return r * g.P + uni((slot_id - r % g.P + g.P) % g.P); };
+    const int j = unit_at(0);
     if (j >= end) return;
 
     const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
@@ -801,9 +813,9 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
 
     Unit u = unit_of<MODE, 0>(g, work, j), un = u;
     copy_list<0>(g, u, list_u(0), wave, lane);
-    bool more = j + g.P < end;
+    bool more = unit_at(1) < end;
     if (more) {
-        un = unit_of<MODE, 0>(g, work, j + g.P);
+        un = unit_of<MODE, 0>(g, work, unit_at(1));
         copy_list<0>(g, un, list_u(1), wave, lane);
     }
     wait_vm_lgkm<0>();
@@ -836,7 +848,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     // the first in address bits 5 and 6
     const uint32_t fc = (uint32_t)((half ^ swz(fr)) * 16);
     const uint32_t wfa = (uint32_t)(GE::kUnit0 + fr * 128) + fc;
-    const uint32_t tfa = (uint32_t)((wm * 128 + fr) * 128) + fc;
+    const uint32_t tfa = (uint32_t)((wm * 32 + fr) * 128) + fc;
     // fragment id (0..3 weights, 4..7 rows) of the stage in row slot n whose
     // weights start at unit w0 of the ring
     auto read = [&](int n, int w0, int kk, int id) {
@@ -845,7 +857,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             wf[kk][id] = frag(lds + at, lds + (at ^ 32u));
         } else {
             const uint32_t at = (tfa ^ (uint32_t)(64 * kk)) + (uint32_t)n * GE::kSlot;
-            const int o = (id - 4) * 4096;
+            const int o = (id - 4) * 8192;
             tf[kk][id - 4] = frag(lds + at + o, lds + (at ^ 32u) + o);
         }
     };
@@ -860,7 +872,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             a[q] = *reinterpret_cast<const u32x4*>(p + (GE::wrow(wn, q) + fr) * 16);
-            b[q] = *reinterpret_cast<const u32x4*>(p + (kTN + wm * 128 + q * 32 + fr) * 16);
+            b[q] = *reinterpret_cast<const u32x4*>(p + (kTN + (2 * q + wm) * 32 + fr) * 16);
         }
         __builtin_amdgcn_sched_barrier(0);  // all reads in flight together
 #pragma unroll
@@ -888,10 +900,10 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             if (more) sc.setup(g, un, list(lists + 1), wave, opaque_v(lane));
             else sc.nothing();
         }
-        sc.copy(lds_u + GE::kScale0, wave);
+        sc.copy(lds_u + GE::kScale0, wave, opaque_v(lane));
     };
     sc.setup(g, u, list(0), wave, lane);
-    sc.copy(lds_u + GE::kScale0, wave);
+    sc.copy(lds_u + GE::kScale0, wave, opaque_v(lane));
     int glen = sc.len;         // stages of this group that are left
     const int gskip = sc.skip;
     for (int n = 0; n < 2; ++n) {
@@ -912,20 +924,21 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     copy_group(0);
     int nlen = sc.len, nskip = sc.skip;  // the group in LDS
     bool refill = false;                 // it has been read: its place is free
-    u32x2 wsn[4], tsn[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) wsn[q] = tsn[q] = u32x2{0, 0};
 
-    for (;;) {
-        f32x16 acc[4][4];
+    Unit u2 = un;
+    bool more2 = false;
+    // One unit whose rows fill NB token blocks of each wave (32 rows of every
+    // 64): its stages and its epilogue.
+    auto run = [&](auto nb_tag) {
+        constexpr int NB = decltype(nb_tag)::value, kM = 4 * NB;  // products per half stage
+        constexpr int kSpread = NB > 2 ? 8 : kM;  // products over which a half's reads are spread
+        f32x16 acc[NB][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][q][v] = 0.0f;
-        Unit u2 = un;
-        bool more2 = false;
         const int KT = GE::stream_stages(u.KT);
         for (int s = 0; s < KT; ++s) {
             // (no branch below this: the compiler would move the first half's
@@ -934,13 +947,18 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
                 // the unit after next: its list goes to the place of the list
                 // of the unit before this one, whose epilogue every wave left
                 // before stage 0's barrier
-                more2 = j + 2 * g.P < end;
+                const int j2 = unit_at(m + 2);
+                more2 = j2 < end;
                 if (more2) {
-                    u2 = unit_of<MODE, 0>(g, work, j + 2 * g.P);
+                    u2 = unit_of<MODE, 0>(g, work, j2);
                     copy_list<0>(g, u2, list_u(m + 2), wave, lane);
                 }
             }
             follow();
+            // the next group's scales; what they hold in other stages is not used
+            u32x2 wsn[4], tsn[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) asm("" : "=v"(wsn[q]), "=v"(tsn[q]));
             if (refill) {  // read by every wave before the last barrier
                 copy_group(m);
                 nlen = sc.len;
@@ -952,25 +970,35 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             }
             const int wnext = wrap(wat + 8), wcopy = wrap(wnext + 8);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
+            for (int q = 0; q < kM; ++q) {
                 acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
-                if (q < 8) read(odd, wat, 1, q);
-                if ((q + 1) * kEarly / 16 > q * kEarly / 16)  // kEarly of them, evenly
-                    cp.weight(q * kEarly / 16, unit_u(wcopy, q * kEarly / 16), wave);
+                // this half's share of the reads (NB row blocks) and copies
+#pragma unroll
+                for (int z = q * 8 / kSpread; z < (q + 1) * 8 / kSpread && z < 4 + NB; ++z) read(odd, wat, 1, z);
+#pragma unroll
+                for (int z = q * kEarly / kM; z < (q + 1) * kEarly / kM; ++z) cp.weight(z, unit_u(wcopy, z), wave);
                 __builtin_amdgcn_sched_barrier(0);
             }
             wait_vm_lgkm<kEarly>();
             slot_barrier();  // the next stage has landed, and this one's slots are free
             const uint32_t sl = slot_u(odd);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
+            for (int q = 0; q < kM; ++q) {
                 acc[q >> 2][q & 3] = mfma<1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
-                if (q < kWCopies - kEarly) cp.weight(kEarly + q, unit_u(wcopy, kEarly + q), wave);
-                else if (q - (kWCopies - kEarly) < GE::kACopies) cp.row(q - (kWCopies - kEarly), sl, wave);
-                if (q >= 2 && q < 10) read(odd ^ 1, wnext, 0, q - 2);
+#pragma unroll
+                for (int z = q * 12 / kM; z < (q + 1) * 12 / kM; ++z) {
+                    if (z < GE::kACopies) cp.row(z, sl, wave);
+                    else if (z - GE::kACopies < kWCopies - kEarly)
+                        cp.weight(kEarly + z - GE::kACopies, unit_u(wcopy, kEarly + z - GE::kACopies), wave);
+                }
+#pragma unroll
+                for (int z = q * 8 / kSpread; z < (q + 1) * 8 / kSpread && z < 8; ++z) read(odd ^ 1, wnext, 0, z);
                 // scales that no product of this stage needs any more
-                if (q % 4 == 3) next_scale(ts[q >> 2], tsn[q >> 2], refill);
-                if (q >= 12) next_scale(ws[q - 12], wsn[q - 12], refill);
+                if (q % 4 == 3 && q < kM - 1) next_scale(ts[q >> 2], tsn[q >> 2], refill);
+                if (q >= kM - 4) next_scale(ws[q - (kM - 4)], wsn[q - (kM - 4)], refill);
+                if (q == kM - 1)
+#pragma unroll
+                    for (int i = NB - 1; i < 4; ++i) next_scale(ts[i], tsn[i], refill);
                 __builtin_amdgcn_sched_barrier(0);
             }
             ++cp.st;
@@ -981,19 +1009,24 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
         drain();
         if (u.pidx >= 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) store_part<MODE, 0>(g, u.pidx, i, acc[i], wave, opaque_v(lane));
+            for (int i = 0; i < NB; ++i) store_part<MODE, 0>(g, u.pidx, i, acc[i], wave, opaque_v(lane));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NB; ++i) {
                 finish<MODE, 0>(g, u, i, acc[i], list(m), wave, opaque_v(lane));
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    };
+    for (;;) {
+        if (u.rows > 192) run(std::integral_constant<int, 4>{});
+        else if (u.rows > 128) run(std::integral_constant<int, 3>{});
+        else if (u.rows > 64) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, 1>{});
         if (!more) break;
         u = un;
         un = u2;
         more = more2;
-        j += g.P;
         ++m;
     }
 }
@@ -1025,7 +1058,7 @@ __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
     tile_of<MODE, KIND>(g, w.full + t, u);
     const int wave = uni((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / GE::WN;
-    if ((wm * GE::TB + i) * 32 >= u.rows) return;
+    if ((i * GE::WM + wm) * 32 >= u.rows) return;
     f32x16 acc[GE::WB];
 #pragma unroll
     for (int j = 0; j < GE::WB; ++j)

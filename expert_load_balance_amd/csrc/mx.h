@@ -68,8 +68,10 @@ inline int64_t mx_part_units(const moe_shape_t& s, int kind)
     const int64_t N = (int64_t)s.T * s.k;
     const int base = mx_base(s);
     if (kind < base) return 0;
+    // experts of this kind, one tile each, and the base kind's further tiles
     int64_t tiles = N / (kind + 1 == kMxKinds ? 1 : mx_rows(kind + 1) + 1);
-    if (kind > base && tiles > s.E) tiles = s.E;  // at most one tail per expert
+    if (tiles > s.E) tiles = s.E;
+    if (kind == base) tiles += N / mx_rows(base);
     const int64_t gu = tiles * (s.F / (kMxTileN / 2)) * (s.H / kMxStage / kMxMinStages);
     const int64_t dn = tiles * ((s.H + kMxTileN - 1) / kMxTileN) * (s.F / kMxStage / kMxMinStages);
     const int64_t u = gu > dn ? gu : dn;
