@@ -28,7 +28,9 @@
 // differs from another's by about one tile whatever the mix.
 //
 // The leftover tiles of a kind past its whole rounds of P are cut along K
-// when there are few rounds (kSplitRounds): each part stores its fp32 tile in
+// when the launch has fewer than kSplitRounds rounds of tiles (on 1.5 rounds
+// of the 8-expert shape's down projection 377 -> 285 us with the fixup; from 4
+// rounds up it gained what the fixup cost): each part stores its fp32 tile in
 // fragment order, and mx_fixup_kernel adds the parts in order and finishes.
 #include <type_traits>
 
@@ -46,7 +48,7 @@ constexpr int kTN = moe::kMxTileN;
 constexpr int kTK = moe::kMxStage;
 constexpr int kWBytes = kTN * kTK;       // 32 KB of weights per stage
 constexpr int kWCopies = kWBytes / 4096; // 16-byte copies per wave per stage
-constexpr int kSplitRounds = 6;
+constexpr int kSplitRounds = 3;
 enum { kGateUp = 0, kDown = 1 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -288,11 +290,11 @@ __device__ __forceinline__ int opaque_v(int v)
 struct KindWork {
     int full, L, S, first, count;
 };
-__device__ __forceinline__ KindWork kind_work(int n, int first, int P, int KT)
+__device__ __forceinline__ KindWork kind_work(int n, int first, int P, int KT, bool split)
 {
     KindWork w{n, 0, 1, first, n};
     const int left = uni(n % P);
-    if (left > 0 && n < kSplitRounds * P) {
+    if (left > 0 && split) {
         const int s0 = uni(min(P / left, KT / moe::kMxMinStages));
         if (s0 > 1) {
             w.S = s0;
@@ -307,6 +309,7 @@ __device__ __forceinline__ KindWork kind_work(int n, int first, int P, int KT)
 struct Unit {
     int e, n0, rows, x0;   // expert, first weight row, rows, first virtual row
     int k0, KT, pidx;      // K-stages k0 .. k0 + KT; partial tile or -1
+    int rot;               // which of them comes first (the others follow, then 0 .. rot - 1)
 };
 
 struct Gemm {
@@ -325,11 +328,15 @@ __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 {
     const int KT = (MODE == kGateUp ? g.H : g.F) / kTK;
     KindWork w{0, 0, 1, 0, 0};
-    int first = 0;
-    for (int k = 0; k <= kind; ++k) {
-        w = kind_work(ldc(g.sched, k * (g.E + 1) + g.E) * g.ntn, first, g.P, KT);
-        first += w.count;
-    }
+    int n[kMxKinds], total = 0, first = 0;
+#pragma unroll
+    for (int k = 0; k < kMxKinds; ++k) total += n[k] = ldc(g.sched, k * (g.E + 1) + g.E) * g.ntn;
+#pragma unroll
+    for (int k = 0; k < kMxKinds; ++k)
+        if (k <= kind) {
+            w = kind_work(n[k], first, g.P, KT, total < kSplitRounds * g.P);
+            first += w.count;
+        }
     return w;
 }
 
@@ -372,6 +379,15 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
         t = w.full + uni(u.pidx % w.L);
     }
     tile_of<MODE, KIND>(g, t, u);
+    // Rows a multiple of 4 KB apart: if every workgroup walked K from the same
+    // stage, the lines in flight would share their low address bits and crowd
+    // a few memory channels, so neighbouring N-tiles start four stages apart
+    // (a whole group of scales; the M-tiles of one N-tile stay in step).
+    // Measured: gate/up of 128 x 16 rows of 4096 x 1536 391 -> 338 us, of 8 x 512
+    // rows of 4096 x 14336 515 -> 486 us. Not done for other strides: on 2 KB and
+    // 7 KB rows it cost 1 to 5 %.
+    const int K = MODE == kGateUp ? g.H : g.F;
+    u.rot = u.pidx < 0 && K % 4096 == 0 ? uni(u.n0 / (MODE == kGateUp ? kTN / 2 : kTN) * 4 % u.KT) : 0;
     return u;
 }
 
@@ -438,6 +454,7 @@ struct Copier {
     uint32_t aoff[GE::kACopies], woff, asoff, wsoff;
     int rows32;        // bytes of 32 weight rows
     bool upper;        // weight blocks 4..7 lie inside the matrix
+    int rot;
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
 
     // list: the unit's row list in LDS (gate/up; down reads h in virtual order)
@@ -452,6 +469,7 @@ struct Copier {
         wb1 = MODE == kGateUp ? uni_ptr((const char*)g.w1 + e0 * K + u.k0 * kTK) : wb0;
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + u.k0 * 4);
         st = 0;
+        rot = u.rot;
         real = u.KT;
         KT = GE::stream_stages(u.KT);
         auto source = [&](int r) { return MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r; };
@@ -475,25 +493,26 @@ struct Copier {
     }
     __device__ __forceinline__ void nothing()
     {
-        st = real = 0;
+        st = real = rot = 0;
         KT = 0x7fffffff;
     }
+    __device__ __forceinline__ int ks() const { return st + rot >= real ? st + rot - real : st + rot; }
     __device__ __forceinline__ uint32_t range() const { return st < real ? kCopyRange : 0u; }
     // The next stage into a slot; each call of row and weight is one
     // instruction, scales is two.
     __device__ __forceinline__ void row(int i, uint32_t slot, int wave) const
     {
-        copy16(buffer_of(ab, range()), aoff[i], st * kTK, slot + wave * 1024 + i * 4096);
+        copy16(buffer_of(ab, range()), aoff[i], ks() * kTK, slot + wave * 1024 + i * 4096);
     }
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
         copy16(buffer_of(i < 4 ? wb0 : wb1, i < 4 || upper ? range() : 0u), woff,
-               st * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
+               ks() * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
-        copy4(buffer_of(sb, range()), wsoff, st * 4, sslot + wave * 256);
-        if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, st * 4, sslot + kTN * 4 + wave * GE::kRows);
+        copy4(buffer_of(sb, range()), wsoff, ks() * 4, sslot + wave * 256);
+        if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, ks() * 4, sslot + kTN * 4 + wave * GE::kRows);
     }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
@@ -559,17 +578,19 @@ __device__ __forceinline__ float4* part_at(const Gemm& g, int pidx, int wave, in
     return reinterpret_cast<float4*>(base) + ((((size_t)wave * GE::TB + i) * GE::WB + j) * 4) * 64 + lane;
 }
 template <int MODE, int KIND>
-__device__ __forceinline__ void store_part(const Gemm& g, int pidx, int i,
+__device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
                                            const f32x16 (&acc)[Geo<MODE, KIND>::WB], int wave, int lane)
 {
+    using GE = Geo<MODE, KIND>;
+    const bool in = (i * GE::WM + wave / GE::WN) * 32 + (lane & 31) < u.rows;  // padding rows are left out
+    const auto to = store_to(part_at<MODE, KIND>(g, u.pidx, wave, i, 0, 0));
 #pragma unroll
-    for (int j = 0; j < Geo<MODE, KIND>::WB; ++j) {
-        float4* dst = part_at<MODE, KIND>(g, pidx, wave, i, j, lane);
+    for (int j = 0; j < GE::WB; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            dst[q * 64] = make_float4(take(acc[j][4 * q]), take(acc[j][4 * q + 1]), take(acc[j][4 * q + 2]),
-                                      take(acc[j][4 * q + 3]));
-    }
+            store16(to, in ? (uint32_t)(((j * 4 + q) * 64 + lane) * 16) : kZeroRow, __float_as_uint(take(acc[j][4 * q])),
+                    __float_as_uint(take(acc[j][4 * q + 1])), __float_as_uint(take(acc[j][4 * q + 2])),
+                    __float_as_uint(take(acc[j][4 * q + 3])));
 }
 
 // ------------------------------------------------- tiles below 256 rows --
@@ -714,7 +735,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
         drain();
         if (u.pidx >= 0) {
 #pragma unroll
-            for (int b = 0; b < GE::TB; ++b) store_part<MODE, KIND>(g, u.pidx, b, acc[b], wave, opaque_v(lane));
+            for (int b = 0; b < GE::TB; ++b) store_part<MODE, KIND>(g, u, b, acc[b], wave, opaque_v(lane));
         } else {
 #pragma unroll
             for (int b = 0; b < GE::TB; ++b) finish<MODE, KIND>(g, u, b, acc[b], list(m), wave, opaque_v(lane));
@@ -765,7 +786,7 @@ struct ScaleStream {
         n0 = u.n0;
         asb = uni_ptr((const char*)g.as + (MODE == kGateUp ? 0 : (size_t)u.x0 * KS));
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + (size_t)u.e * wrows * KS);
-        at = u.k0;
+        at = u.k0 + u.rot;
         left = Geo<MODE, 0>::stream_stages(u.KT);
         KT_all = K / kTK;
         const int r = 64 * wave + lane;
@@ -788,6 +809,7 @@ struct ScaleStream {
         copy16(buffer_of(sb, kCopyRange), wsoff, from * 4, lds + wave * 1024);
         copy16(buffer_of(asb, kCopyRange), asoff, from * 4, lds + kTN * 16 + wave * 1024);
         at += len;
+        if (at == KT_all) at = 0;  // (only where the unit began past 0)
         left -= len;
     }
 };
@@ -1009,7 +1031,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
         drain();
         if (u.pidx >= 0) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) store_part<MODE, 0>(g, u.pidx, i, acc[i], wave, opaque_v(lane));
+            for (int i = 0; i < NB; ++i) store_part<MODE, 0>(g, u, i, acc[i], wave, opaque_v(lane));
         } else {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -1045,7 +1067,20 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 
 // Adds the K-parts of split tiles in order: workgroup (tile, token block) of
 // a kind, its waves as the tile's.
-constexpr int kFixTiles = moe::kGemmMaxGrid / 2;  // most split tiles of a kind (S >= 2)
+//
+// fix_items: the most (tile, block) pairs of a kind that the launch can have
+// to finish: fewer than P tiles are split, no more than it can have at all,
+// and no expert has more rows than there are tokens.
+inline int fix_items(const moe_shape_t& s, int mode, int kind, int P)
+{
+    const int base = moe::mx_base(s), tb = kind == 0 ? 4 : mx_rows(kind) / 32;
+    const int KT = (mode == kGateUp ? s.H : s.F) / kTK;
+    if (kind < base || KT < 2 * moe::kMxMinStages) return 0;
+    if (kind < kMxKinds - 1 && s.T <= mx_rows(kind + 1)) return 0;
+    const int ntn = mode == kGateUp ? s.F / (kTN / 2) : (s.H + kTN - 1) / kTN;
+    const int64_t tiles = moe::mx_tiles(s, kind) * ntn;
+    return (int)(tiles < P ? tiles : P) * tb;
+}
 
 template <int MODE, int KIND>
 __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
@@ -1064,7 +1099,8 @@ __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
     for (int j = 0; j < GE::WB; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
-    for (int p = 0; p < w.S; ++p)
+    const int last = (i * GE::WM + wm) * 32 + (lane & 31) < u.rows ? w.S : 0;  // padding rows have no parts
+    for (int p = 0; p < last; ++p)
 #pragma unroll
         for (int j = 0; j < GE::WB; ++j) {
             const float4* src = part_at<MODE, KIND>(g, p * w.L + t, wave, i, j, lane);
@@ -1080,17 +1116,29 @@ __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
     finish<MODE, KIND>(g, u, i, acc, g.vrow + u.x0, wave, lane);
 }
 
-constexpr int kFix0 = kFixTiles * 4, kFix1 = kFix0 + kFixTiles * 4, kFix2 = kFix1 + kFixTiles * 2,
-              kFix3 = kFix2 + kFixTiles;
+struct FixGrid {
+    int end[kMxKinds];
+};
 
 template <int MODE>
-__global__ __launch_bounds__(kThreads) void mx_fixup_kernel(const Gemm g)
+__global__ __launch_bounds__(kThreads) void mx_fixup_kernel(const Gemm g, const FixGrid f)
 {
     const int b = blockIdx.x;
-    if (b < kFix0) fix_tile<MODE, 0>(g, b);
-    else if (b < kFix1) fix_tile<MODE, 1>(g, b - kFix0);
-    else if (b < kFix2) fix_tile<MODE, 2>(g, b - kFix1);
-    else fix_tile<MODE, 3>(g, b - kFix2);
+    if (b < f.end[0]) fix_tile<MODE, 0>(g, b);
+    else if (b < f.end[1]) fix_tile<MODE, 1>(g, b - f.end[0]);
+    else if (b < f.end[2]) fix_tile<MODE, 2>(g, b - f.end[1]);
+    else fix_tile<MODE, 3>(g, b - f.end[2]);
+}
+
+template <int MODE>
+hipError_t launch_fixup(const Gemm& g, const moe_shape_t& s, hipStream_t st)
+{
+    FixGrid f;
+    int n = 0;
+    for (int k = 0; k < kMxKinds; ++k) f.end[k] = n += fix_items(s, MODE, k, g.P);
+    if (n == 0) return hipSuccess;
+    mx_fixup_kernel<MODE><<<n, kThreads, 0, st>>>(g, f);
+    return hipGetLastError();
 }
 
 // One workgroup per CU, a multiple of 8 (as many on every XCD), at most what
@@ -1143,8 +1191,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.s1 = w.up_s;
     gemm_mx_kernel<kGateUp><<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    mx_fixup_kernel<kGateUp><<<kFix3, kThreads, 0, st>>>(g);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_fixup<kGateUp>(g, s, st)) != hipSuccess) return e;
     g.ntn = (s.H + kTN - 1) / kTN;
     g.a = g.h;
     g.as = g.hs;
@@ -1153,6 +1200,5 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.w1 = g.s1 = nullptr;
     gemm_mx_kernel<kDown><<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    mx_fixup_kernel<kDown><<<kFix3, kThreads, 0, st>>>(g);
-    return hipGetLastError();
+    return launch_fixup<kDown>(g, s, st);
 }

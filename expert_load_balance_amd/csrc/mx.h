@@ -60,18 +60,25 @@ __host__ __device__ constexpr int mx_rows(int kind) { return 256 >> kind; }
 // bytes (512 values of K) at a time.
 __host__ inline int mx_base(const moe_shape_t& s) { return s.H >= 512 && s.F >= 512 ? 0 : 1; }
 
-// Upper bound on the K-parts of one kind in one launch: no more than the
-// workgroups, and than the tiles that N rows of E experts can make, cut into
-// parts of kMxMinStages.
-inline int64_t mx_part_units(const moe_shape_t& s, int kind)
+// Upper bound on the tiles of one kind: experts of this kind, one tile each,
+// and the base kind's further tiles.
+inline int64_t mx_tiles(const moe_shape_t& s, int kind)
 {
     const int64_t N = (int64_t)s.T * s.k;
     const int base = mx_base(s);
     if (kind < base) return 0;
-    // experts of this kind, one tile each, and the base kind's further tiles
     int64_t tiles = N / (kind + 1 == kMxKinds ? 1 : mx_rows(kind + 1) + 1);
     if (tiles > s.E) tiles = s.E;
-    if (kind == base) tiles += N / mx_rows(base);
+    return kind == base ? tiles + N / mx_rows(base) : tiles;
+}
+
+// Upper bound on the K-parts of one kind in one launch: no more than the
+// workgroups (more parts than that, up to three rounds of them, were no faster
+// on one decoded token's 96 tiles), and than its tiles cut into parts of
+// kMxMinStages.
+inline int64_t mx_part_units(const moe_shape_t& s, int kind)
+{
+    const int64_t tiles = mx_tiles(s, kind);
     const int64_t gu = tiles * (s.F / (kMxTileN / 2)) * (s.H / kMxStage / kMxMinStages);
     const int64_t dn = tiles * ((s.H + kMxTileN - 1) / kMxTileN) * (s.F / kMxStage / kMxMinStages);
     const int64_t u = gu > dn ? gu : dn;
