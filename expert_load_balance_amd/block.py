@@ -10,6 +10,7 @@ bytes). Tensors have to lie on the current device.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import expert_load_balance_amd as _moe
 
@@ -30,6 +31,7 @@ BLOCK_SYMBOLS = (
 MX_BLOCK = 32
 
 _VP = ctypes.c_void_p
+_dtype_of = operator.attrgetter("dtype")
 
 
 class GradT(ctypes.Structure):
@@ -199,23 +201,26 @@ def _columns(ts, other, here, what):
     """(addresses, element counts, moe_dtypes) of a list of gradients. The
     checks are the single pointer's, a column at a time: a step has hundreds of
     tensors."""
+    import torch
+
+    T = torch.Tensor
     _, acts, _, _, _, _ = _env()
     f32, bf = acts[_moe.MOE_F32][0], acts[_moe.MOE_BF16][0]
-    try:
-        dts = [t.dtype for t in ts]
-        ok = (all([t.get_device() == here for t in ts]) and all([t.is_contiguous() for t in ts])
-              and all([d is f32 or d is bf for d in dts]))
+    try:  # mapped methods cost two thirds of a loop's
+        dts = list(map(_dtype_of, ts))
+        count = list(map(T.numel, ts))
+        ok = (set(map(T.get_device, ts)) <= {here} and all(map(T.is_contiguous, ts))
+              and set(dts) <= {f32, bf})
         if ok and other is not None:
-            ok = dts == [t.dtype for t in other] and [t.numel() for t in ts] == [t.numel() for t in other]
-    except AttributeError:
+            ok = dts == list(map(_dtype_of, other)) and count == list(map(T.numel, other))
+    except (TypeError, AttributeError):
         ok = False
     if not ok:
         for i, t in enumerate(ts):
             _ptr(t, (f32, bf), f"{what} {i}", 0, here)
             if other is not None and (t.dtype != other[i].dtype or t.numel() != other[i].numel()):
                 raise ValueError(f"{what} {i} differs from its gradient in type or size")
-    return ([t.data_ptr() for t in ts], [t.numel() for t in ts],
-            [_moe.MOE_BF16 if d is bf else _moe.MOE_F32 for d in dts])
+    return list(map(T.data_ptr, ts)), count, [_moe.MOE_BF16 if d is bf else _moe.MOE_F32 for d in dts]
 
 
 def _grad_list(grads, into, here):

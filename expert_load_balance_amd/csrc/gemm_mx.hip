@@ -237,20 +237,20 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t rsrc, uint32_t of
 __device__ __forceinline__ void store_h(const f32x16& g, const f32x16& u, __amdgpu_buffer_rsrc_t h, uint32_t off,
                                         __amdgpu_buffer_rsrc_t hs, uint32_t soff, int half)
 {
-    float hv[16], top = 0.0f;
+    float hv[16];
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         hv[i] = fast_silu(take(g[i])) * take(u[i]);
-        top = fmaxf(top, moe::mx_abs(hv[i]));
+        top = max(top, moe::mx_mag(hv[i]));
     }
-    uint32_t t0 = __float_as_uint(top), t1 = t0;
+    uint32_t t0 = top, t1 = top;
     swap32(t0, t1);
-    const uint32_t byte = moe::mx_scale_byte(fmaxf(__uint_as_float(t0), __uint_as_float(t1)));
-    const float inv = moe::mx_inv_scale(byte);
+    const uint32_t byte = moe::mx_scale_byte(max(t0, t1));
     uint32_t w[4];  // w[i]: columns 8 i + 4 half ..
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = moe::mx_pack4(hv[4 * i] * inv, hv[4 * i + 1] * inv, hv[4 * i + 2] * inv, hv[4 * i + 3] * inv);
+        w[i] = moe::mx_pack4(hv[4 * i], hv[4 * i + 1], hv[4 * i + 2], hv[4 * i + 3], byte);
     swap32(w[0], w[2]);  // lower lanes: columns 0..3, 4..7; upper: 16..19, 20..23
     swap32(w[1], w[3]);
     store16(h, off, w[0], w[2], w[1], w[3]);

@@ -10,42 +10,34 @@ namespace moe {
 
 constexpr int kMxBlock = 32;
 
-// Scale byte of a block whose largest magnitude is `top`: the smallest e >=
-// -127 with top <= 448 * 2^e = 1.75 * 2^(e + 8), as e + 127. With top =
-// m * 2^x, m in [1, 2), e is x - 8 where m <= 1.75, else x - 7: adding
-// 0x1fffff to the bits carries into the exponent exactly when the mantissa
-// field exceeds 0x600000 (m > 1.75). Infinities and NaN give 255.
-__device__ __forceinline__ uint32_t mx_scale_byte(float top)
+// Scale byte of a block whose largest magnitude has the bits `top`: the
+// smallest e >= -127 with top <= 448 * 2^e = 1.75 * 2^(e + 8), as e + 127.
+// With top = m * 2^x, m in [1, 2), e is x - 8 where m <= 1.75, else x - 7:
+// adding 0x1fffff to the bits carries into the exponent exactly when the
+// mantissa field exceeds 0x600000 (m > 1.75). Infinities and NaN give 255.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top)
 {
-    const uint32_t b = __float_as_uint(top) & 0x7fffffffu;
-    if (b >= 0x7f800000u) return 255u;
-    const int e = (int)((b + 0x1fffffu) >> 23) - 8;
-    return (uint32_t)(e > 0 ? e : 0);
+    const int e = (int)((top + 0x1fffffu) >> 23) - 8;
+    return top >= 0x7f800000u ? 255u : (uint32_t)(e > 0 ? e : 0);
 }
 
-// 2^-e of that byte, exact: bits of 2^(127 - byte). Bytes 0..253 occur with
-// finite blocks (at most 247); 255 gives NaN, which makes every code NaN.
-__device__ __forceinline__ float mx_inv_scale(uint32_t byte)
+// Four e4m3 codes of values divided by the block's scale (its byte as an
+// exponent; the division is exact), first in the low byte. The quotients are
+// at most 448 in magnitude, so the conversion (to nearest even) never
+// saturates; a scale byte of 255 makes every code NaN.
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d, uint32_t byte)
 {
-    if (byte == 255u) return __uint_as_float(0x7fc00000u);
-    return __uint_as_float((254u - byte) << 23);
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float s = __uint_as_float(byte << 23);
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, s, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, s, true);
+    return __builtin_bit_cast(uint32_t, r);
 }
 
-// Four e4m3 codes, first in the low byte. The quotients are at most 448 in
-// magnitude, so the conversion (to nearest even) never saturates.
-__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d)
-{
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-}
-
-// |v| for a block maximum. fmaxf drops a NaN operand; a NaN becomes an
-// infinity here so that its block is still seen to hold one.
-__device__ __forceinline__ float mx_abs(float v)
-{
-    const float a = fabsf(v);
-    return a == a ? a : __uint_as_float(0x7f800000u);
-}
+// Bits of |v|, for a block maximum taken over unsigned integers: they order
+// as the magnitudes do, infinities above every number and NaN above those.
+__device__ __forceinline__ uint32_t mx_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // 8-bit GEMM geometry: a workgroup tile is 256, 128, 64 or 32 rows (kinds 0..3)
 // x 256 weight rows (gate/up: 128 of each), K in stages of 128 bytes (four

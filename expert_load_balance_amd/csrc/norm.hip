@@ -98,17 +98,16 @@ template <bool BF16>
 __device__ __forceinline__ void store_mx(const float* v, int64_t vec, bool in, uint8_t* q, uint8_t* scales)
 {
     constexpr int N = Vec<BF16>::kN, kLanes = moe::kMxBlock / N;
-    float top = 0.0f;
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) top = fmaxf(top, moe::mx_abs(v[k]));
+    for (int k = 0; k < N; ++k) top = max(top, moe::mx_mag(v[k]));
 #pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+    for (int off = 1; off < kLanes; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
     const uint32_t byte = moe::mx_scale_byte(top);
-    const float inv = moe::mx_inv_scale(byte);
     uint32_t w[N / 4];
 #pragma unroll
     for (int k = 0; k < N / 4; ++k)
-        w[k] = moe::mx_pack4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+        w[k] = moe::mx_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], byte);
     if (!in) return;
     if (BF16) *reinterpret_cast<uint2*>(q + vec * 8) = make_uint2(w[0], w[N / 4 - 1]);
     else *reinterpret_cast<uint32_t*>(q + vec * 4) = w[0];
