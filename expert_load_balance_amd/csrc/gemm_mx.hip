@@ -1069,14 +1069,15 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 // a kind, its waves as the tile's.
 //
 // fix_items: the most (tile, block) pairs of a kind that the launch can have
-// to finish: fewer than P tiles are split, no more than it can have at all,
-// and no expert has more rows than there are tokens.
+// to finish: fewer than P tiles are split, and no more than it can have at
+// all. (An expert can hold every assignment, not one of each token only: ids
+// that name it twice are flagged by the count, and computed.)
 inline int fix_items(const moe_shape_t& s, int mode, int kind, int P)
 {
     const int base = moe::mx_base(s), tb = kind == 0 ? 4 : mx_rows(kind) / 32;
     const int KT = (mode == kGateUp ? s.H : s.F) / kTK;
     if (kind < base || KT < 2 * moe::kMxMinStages) return 0;
-    if (kind < kMxKinds - 1 && s.T <= mx_rows(kind + 1)) return 0;
+    if (kind < kMxKinds - 1 && (int64_t)s.T * s.k <= mx_rows(kind + 1)) return 0;
     const int ntn = mode == kGateUp ? s.F / (kTN / 2) : (s.H + kTN - 1) / kTN;
     const int64_t tiles = moe::mx_tiles(s, kind) * ntn;
     return (int)(tiles < P ? tiles : P) * tb;

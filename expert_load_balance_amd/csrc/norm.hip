@@ -7,12 +7,15 @@
 // Bound by memory: each input is read once and each output written once. One
 // workgroup takes one row and keeps it in registers between the sum of
 // squares and the outputs, as CH 16-byte vectors per thread.
+#include <type_traits>
+
 #include "mx.h"
 
 namespace {
 
 constexpr int kMaxCh = 4;          // vectors per thread on the register path
 constexpr int kMaxThreads = 1024;
+constexpr int kMaxRows = 1 << 21;  // workgroups of a launch: of kMaxThreads each, half of the 2^32 threads it can hold
 constexpr int kRedCols = 64;       // columns per workgroup of the dweight sum
 
 template <bool BF16>
@@ -334,12 +337,12 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_bwd_wide_kernel(
 
 // dweight[h] = sum over the workgroups' rows of part, in a fixed order: 16
 // threads per column take every 16th row, then their sums are added in order.
-__global__ __launch_bounds__(1024) void dweight_kernel(int G, int H, const float* __restrict__ part,
+__global__ __launch_bounds__(1024) void dweight_kernel(int G, int H, int h0, const float* __restrict__ part,
                                                        float* __restrict__ dweight)
 {
     __shared__ float sh[16][kRedCols];
     const int col = threadIdx.x % kRedCols, grp = threadIdx.x / kRedCols;
-    const int h = blockIdx.x * kRedCols + col;
+    const int h = h0 + blockIdx.x * kRedCols + col;
     float a = 0.0f;
     if (h < H) {
         int g = grp;
@@ -453,10 +456,25 @@ hipError_t moe_launch_rmsnorm(const moe_shape_t& s, const void* x, const void* r
                               const void* weight, float eps, void* s_out, void* y, void* q,
                               void* scales, float* rstd, hipStream_t st)
 {
-    if (s.T == 0) return hipSuccess;
-    return s.dtype == MOE_BF16
-               ? launch_norm<true>(s, x, residual, weight, eps, s_out, y, q, scales, rstd, st)
-               : launch_norm<false>(s, x, residual, weight, eps, s_out, y, q, scales, rstd, st);
+    // (past 2^32 threads a launch quietly runs the remainder only)
+    moe_shape_t part = s;
+    for (int64_t t0 = 0; t0 < s.T; t0 += kMaxRows) {
+        part.T = (int)(s.T - t0 < kMaxRows ? s.T - t0 : kMaxRows);
+        auto at = [&](auto* p, int64_t row_bytes) {
+            using Byte = std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(p)>>, const char, char>;
+            return p ? static_cast<decltype(p)>(static_cast<Byte*>(p) + t0 * row_bytes) : nullptr;
+        };
+        const int64_t row = (int64_t)s.H * (s.dtype == MOE_BF16 ? 2 : 4);
+        float* rs = rstd ? rstd + t0 : nullptr;
+        const hipError_t e =
+            s.dtype == MOE_BF16
+                ? launch_norm<true>(part, at(x, row), at(residual, row), weight, eps, at(s_out, row), at(y, row),
+                                    at(q, s.H), at(scales, s.H / moe::kMxBlock), rs, st)
+                : launch_norm<false>(part, at(x, row), at(residual, row), weight, eps, at(s_out, row), at(y, row),
+                                     at(q, s.H), at(scales, s.H / moe::kMxBlock), rs, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t moe_launch_rmsnorm_backward(const moe_shape_t& s, const void* s_in, const void* weight,
@@ -470,8 +488,13 @@ hipError_t moe_launch_rmsnorm_backward(const moe_shape_t& s, const void* s_in, c
                                  : launch_norm_bwd<false>(s, s_in, weight, rstd, dy, ds, dx, part, G, st);
         if (e != hipSuccess) return e;
     }
-    dweight_kernel<<<(s.H + kRedCols - 1) / kRedCols, 1024, 0, st>>>(G, s.H, part, dweight);
-    return hipGetLastError();
+    for (int64_t h0 = 0; h0 < s.H; h0 += (int64_t)kMaxRows * kRedCols) {
+        const int64_t left = (s.H - h0 + kRedCols - 1) / kRedCols;
+        dweight_kernel<<<(int)(left < kMaxRows ? left : kMaxRows), 1024, 0, st>>>(G, s.H, (int)h0, part, dweight);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t moe_launch_mx_quantize(int64_t rows, int64_t cols, int dtype, const void* x, void* q,

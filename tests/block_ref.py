@@ -65,7 +65,7 @@ def check_blocks(q, s, v, d, what):
     unit = torch.exp2(s.double() - 127)[..., None]
     # half a step: 2^-4 of a normal value, 2^-10 of the scale below those
     tol = torch.maximum(b.abs() * 2.0 ** -4, unit * 2.0 ** -10) + t
-    bad = (got - b).abs() > tol * (1 + 1e-12)
+    bad = ~((got - b).abs() <= tol * (1 + 1e-12))
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} codes further than half a step"
 
 

@@ -115,6 +115,21 @@ def test_rmsnorm_outputs_one_by_one_and_in_place():
         assert torch.equal(b, full["y"]) and torch.equal(a, x)
 
 
+def test_rmsnorm_more_rows_than_one_launch_takes():
+    """2^26 + 3 rows of 64 threads each are more threads than a launch holds."""
+    T, H = (1 << 26) + 3, 4
+    x = torch.zeros(T, H, device=DEV)
+    some = torch.tensor([0, 1, (1 << 21) - 1, 1 << 21, (1 << 25) + 7, T - 1], device=DEV)
+    g = gen(4)
+    x[some], w = randn(g, len(some), H), 1 + 0.1 * randn(g, H)
+    y, rstd = torch.full_like(x, 9.0), torch.zeros(T, device=DEV)
+    moe.moe_rmsnorm(norm_shape(T, H, F32), x, w, EPS, y=y, rstd=rstd)
+    _, rr, v = ref.norm(x[some], None, w, EPS)
+    assert bool(((y[some].double() - v).abs() <= v.abs() * (ref.norm_rel(H) + ref.HALF[F32])).all())
+    assert bool(((rstd[some].double() - rr).abs() <= rr * ref.norm_rel(H)).all())
+    assert int((y != 0).any(-1).sum()) == len(some) and bool((rstd > 0).all())
+
+
 def test_rmsnorm_nonfinite_rows_stay_apart():
     T, H = 6, 256
     g = gen(5)
@@ -305,7 +320,7 @@ def check_layer(L, xq, xs, ids, w, wts):
     assert torch.equal(torch.sort(rows).values, torch.arange(T * k, device=DEV))
     assert torch.equal(L.buf_q[rows], xq.view(torch.uint8)[tok]) and torch.equal(L.buf_s[rows], xs.view(torch.uint8)[tok])
     got = L.y[rows].double()
-    bad = (got - y).abs() > (y.abs() + tol) * ref.HALF[BF] + tol + 1e-30
+    bad = ~((got - y).abs() <= (y.abs() + tol) * ref.HALF[BF] + tol + 1e-30)      # (a NaN is bad)
     assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} values of y, worst {float(((got - y).abs() / (tol + y.abs() * 2.0 ** -8 + 1e-30)).max()):.3g}"
     # (the bound says something: beside the values it is small)
     print("bound / y", float(tol.norm() / y.norm()), "error / y", float((got - y).norm() / y.norm()), flush=True)
@@ -325,6 +340,8 @@ MX_CASES = [
     # 256-row tiles (H and F from 512 up), K of 4 to 9 stages, tails of each size
     (300, 512, 1, 1, 640, 1, 0.0, None), (900, 640, 3, 2, 768, 3, 0.3, None), (1100, 896, 4, 1, 1152, 2, 0.1, None),
     (530, 768, 2, 2, 512, 2, 0.0, None), (2100, 1152, 6, 2, 896, 3, 0.5, [0, 2, 3, 5]), (256, 1280, 1, 1, 512, 1, 0.0, None),
+    # tiles of every kind in one launch, K-parts in each
+    (600, 1024, 24, 2, 1536, 8, 1.5, None),
 ]
 
 
@@ -348,6 +365,35 @@ def test_experts_mx(case):
     L.mx_ws.fill_(0x7F)
     L.experts(xq, xs, ids, w, *wts)
     assert torch.equal(L.out, again) and torch.equal(L.y, y)       # whatever the workspace held
+
+
+@pytest.mark.parametrize("case", [(4200, 2, 4096), (280, 40, 1024)], ids=["256-row tiles", "32-row tiles"])
+def test_experts_mx_rows_4_kb_apart(case):
+    """Whole rounds of tiles on rows a multiple of 4 KB apart, whose K starts
+    are staggered: every row is written, and a sample of them (each tile's ends
+    and its middle) is the float64 experts'."""
+    T, E, F = case
+    H = 4096
+    say("experts_mx", case)
+    g = gen(T)
+    L = MoeLayerMx(moe.Shape(T, H, E, 1, F, 2, 1, moe.MOE_BF16), DEV)
+    xq, xs = quantized(randn(g, T, H))
+    ids, w = choose(g, T, E, 1, 0.0)
+    wts = weights(g, E, F, H)
+    L.y.fill_(float("nan"))
+    L.experts(xq, xs, ids, w, *wts)
+    torch.cuda.synchronize()
+    assert int(L.err.item()) == 0 and bool(torch.isfinite(L.y).all())
+    row = L.dest_row.reshape(-1).long()
+    tok = torch.sort(row).indices[torch.cat([torch.arange(i, T, 64, device=DEV) for i in (0, 31, 63)])]
+    a = ref.values(xq[tok], xs[tok])
+    y, tol = ref.experts(a, xs[tok], ids[tok, 0].long(), *wts)
+    got = L.y[row[tok]].double()
+    assert bool(((got - y).abs() <= (y.abs() + tol) * ref.HALF[BF] + tol + 1e-30).all())
+    # the bound adds F magnitudes where y adds F values of either sign, so
+    # beside y it grows with sqrt(F): check_layer's 0.25, which holds for F up
+    # to 1536, is 0.25 sqrt(4096 / 1536) = 0.41 here
+    assert float(tol.norm()) <= 0.25 * max(1.0, math.sqrt(F / 1536)) * float(y.norm())
 
 
 def test_experts_mx_scales_far_apart():
@@ -384,6 +430,41 @@ def test_experts_mx_nan_stays_in_its_row():
     assert bool(torch.isnan(got[40]).all()) and bool(torch.isnan(got[60]).all())
 
 
+def test_experts_mx_of_refused_ids():
+    """Ids that the count flags: an expert named by every choice of a token
+    (it then has more rows than there are tokens), and ids out of range, whose
+    rows are left out of the sum."""
+    T, H, E, k, F = 40, 1024, 4, 4, 1024
+    g = gen(12)
+    xq, xs = quantized(randn(g, T, H))
+    wts = weights(g, E, F, H)
+    _, w = choose(g, T, E, k, 0.0)
+    L = MoeLayerMx(moe.Shape(T, H, E, k, F, 2, 1, moe.MOE_BF16), DEV)
+    ids = torch.full((T, k), 2, dtype=torch.int32, device=DEV)
+    L.y.fill_(float("nan"))
+    L.experts(xq, xs, ids, w, *wts)
+    torch.cuda.synchronize()
+    assert int(L.err.item()) == moe.ERR_REPEAT
+    L.err.zero_()
+    check_layer(L, xq, xs, ids, w, wts)
+    # out of range: the rest of the token's choices count
+    ids, w = choose(g, T, E, k, 0.0)
+    ids[:, 1], ids[7, 3] = -1, E
+    L.y.fill_(float("nan"))
+    out = L.experts(xq, xs, ids, w, *wts).double()
+    torch.cuda.synchronize()
+    assert int(L.err.item()) == moe.ERR_RANGE
+    flat, tok = ids.reshape(-1).long(), torch.arange(T * k, device=DEV) // k
+    kept = (flat >= 0) & (flat < E)
+    assert torch.equal(L.dest_row.reshape(-1) >= 0, kept)
+    a = ref.values(xq, xs)[tok[kept]]
+    y, tol = ref.experts(a, xs[tok[kept]], flat[kept], *wts)
+    y, tol, ww = y, tol + y.abs() * ref.HALF[BF], w.reshape(-1)[kept].double()[:, None]
+    want = torch.zeros(T, H, dtype=torch.float64, device=DEV).index_add_(0, tok[kept], y * ww)
+    room = torch.zeros_like(want).index_add_(0, tok[kept], tol * ww + (y * ww).abs() * 8 * ref.U)
+    assert bool(((out - want).abs() <= (want.abs() + room) * ref.HALF[BF] + room + 1e-30).all())
+
+
 def test_experts_mx_without_tokens():
     L = MoeLayerMx(moe.Shape(0, 128, 4, 2, 128, 2, 1, moe.MOE_BF16), DEV)
     wts = weights(gen(1), 4, 128, 128)
@@ -412,6 +493,25 @@ def test_rows_behind_the_last_are_left():
     x, wn = randn(g, T, H).to(BF), torch.ones(H, dtype=BF, device=DEV)
     moe.moe_rmsnorm(norm_shape(T, H, BF), x, wn, EPS, s=s, y=y, rstd=rstd)
     assert bool((s[T:] == 9).all()) and bool((y[T:] == 9).all()) and bool((rstd[T:] == 9).all())
+
+
+def test_rmsnorm_backward_of_a_very_wide_row():
+    """2^28 + 64 columns: 16 threads a column are more than a launch holds."""
+    H = (1 << 28) + 64
+    s, w, dy = (torch.zeros(1, H, device=DEV) for _ in range(3))
+    some = torch.tensor([0, 5, (1 << 27) - 1, 1 << 27, (1 << 28) - 1, 1 << 28, H - 1], device=DEV)
+    g = gen(6)
+    for v in (s, w, dy):
+        v[0, some] = 1 + randn(g, len(some)).abs()
+    rstd = torch.full((1,), 0.5, device=DEV)
+    sh = norm_shape(1, H, F32)
+    dw = torch.full((H,), 9.0, device=DEV)
+    ws = torch.empty(moe.moe_rmsnorm_backward_workspace_bytes(sh), dtype=torch.uint8, device=DEV)
+    dx = torch.empty_like(s)
+    moe.moe_rmsnorm_backward(sh, s, w, rstd, dy, dx, dw, ws)
+    want = dy[0, some].double() * s[0, some].double() * 0.5
+    assert bool(((dw[some].double() - want).abs() <= want * 4 * ref.U).all())
+    assert int((dw != 0).sum()) == len(some) and int((dx != 0).sum()) == len(some)
 
 
 # ------------------------------------------------------- gradient norm, clip ----
