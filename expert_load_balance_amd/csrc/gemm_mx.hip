@@ -49,6 +49,7 @@ constexpr int kTK = moe::kMxStage;
 constexpr int kWBytes = kTN * kTK;       // 32 KB of weights per stage
 constexpr int kWCopies = kWBytes / 4096; // 16-byte copies per wave per stage
 constexpr int kSplitRounds = 3;
+constexpr int kPieces = 4;               // of an expert, loaded ahead of their number
 enum { kGateUp = 0, kDown = 1 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -63,41 +64,55 @@ __global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int
                                                                int32_t* __restrict__ sched,
                                                                int32_t* __restrict__ vrow)
 {
-    __shared__ int32_t sh[kMxKinds + 1][kThreads];
+    __shared__ int32_t sum[kMxKinds + 1][kThreads / 64];
     __shared__ int32_t rs[kThreads + 1];
     const moe::PlanLayout L = moe::plan_layout(E, R);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int c = 0;
     if (tid < E) {
+        // (the first pieces are loaded beside their number, which says how many count)
+        int n[kPieces];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) n[p] = p < R ? plan[L.piece_cnt + (size_t)tid * R + p] : 0;
         const int np = plan[L.piece_num + tid];
-        for (int p = 0; p < np && p < R; ++p) c += plan[L.piece_cnt + (size_t)tid * R + p];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) c += p < np ? n[p] : 0;
+        for (int p = kPieces; p < np && p < R; ++p) c += plan[L.piece_cnt + (size_t)tid * R + p];
     }
     // an expert's rows are of one kind: whole tiles and a tail of kind `base`,
     // or, where they fit a smaller tile, one of that kind
+    int v[kMxKinds + 1];
 #pragma unroll
     for (int k = 0; k < kMxKinds; ++k) {
         const int below = k + 1 < kMxKinds ? mx_rows(k + 1) : 0;
         const bool mine = k < base ? false : k == base ? c > below : c > below && c <= mx_rows(k);
-        sh[k][tid] = mine ? (c + mx_rows(k) - 1) / mx_rows(k) : 0;
+        v[k] = mine ? (c + mx_rows(k) - 1) / mx_rows(k) : 0;
     }
-    sh[kMxKinds][tid] = c;
+    v[kMxKinds] = c;
+    // inclusive prefixes: within the waves, then the waves before
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+#pragma unroll
+        for (int q = 0; q <= kMxKinds; ++q) {
+            const int up = __shfl_up(v[q], off);
+            v[q] += lane >= off ? up : 0;
+        }
+    if (lane == 63)
+#pragma unroll
+        for (int q = 0; q <= kMxKinds; ++q) sum[q][wave] = v[q];
     __syncthreads();
-    for (int off = 1; off < kThreads; off <<= 1) {
-        int a[kMxKinds + 1];
 #pragma unroll
-        for (int q = 0; q <= kMxKinds; ++q) a[q] = tid >= off ? sh[q][tid - off] : 0;
-        __syncthreads();
+    for (int w = 0; w < kThreads / 64 - 1; ++w)
 #pragma unroll
-        for (int q = 0; q <= kMxKinds; ++q) sh[q][tid] += a[q];
-        __syncthreads();
-    }
+        for (int q = 0; q <= kMxKinds; ++q) v[q] += w < wave ? sum[q][w] : 0;
     if (blockIdx.x == 0)
+#pragma unroll
         for (int q = 0; q <= kMxKinds; ++q) {
             if (tid == 0) sched[q * (E + 1)] = 0;
-            if (tid < E) sched[q * (E + 1) + tid + 1] = sh[q][tid];
+            if (tid < E) sched[q * (E + 1) + tid + 1] = v[q];
         }
     if (tid == 0) rs[0] = 0;
-    rs[tid + 1] = sh[kMxKinds][tid];
+    rs[tid + 1] = v[kMxKinds];
     __syncthreads();
     const int x = blockIdx.x * kThreads + tid;
     if (x >= N) return;
@@ -107,16 +122,25 @@ __global__ __launch_bounds__(kThreads) void mx_schedule_kernel(int E, int R, int
         if (rs[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
-    const int v = x - rs[lo];
+    const int at = x - rs[lo];
+    int n[kPieces], r0[kPieces];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        n[p] = p < R ? plan[L.piece_cnt + (size_t)lo * R + p] : 0;
+        r0[p] = p < R ? plan[L.piece_row + (size_t)lo * R + p] : 0;
+    }
     const int np = plan[L.piece_num + lo];
-    int cum = 0, row = 0;
-    for (int p = 0; p < np && p < R; ++p) {
-        const int n = plan[L.piece_cnt + (size_t)lo * R + p];
-        if (v < cum + n) {
-            row = plan[L.piece_row + (size_t)lo * R + p] + (v - cum);
-            break;
+    int cum = 0, row = -1;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+        if (p < np) {
+            if (row < 0 && at < cum + n[p]) row = r0[p] + (at - cum);
+            cum += n[p];
         }
-        cum += n;
+    for (int p = kPieces; p < np && p < R && row < 0; ++p) {
+        const int m = plan[L.piece_cnt + (size_t)lo * R + p];
+        if (at < cum + m) row = plan[L.piece_row + (size_t)lo * R + p] + (at - cum);
+        cum += m;
     }
     // (rows past the plan's total, or a damaged plan, stay in the buffer)
     vrow[x] = row >= 0 && row < N ? row : 0;
@@ -340,8 +364,22 @@ __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
     return w;
 }
 
-// Tile t of the kind: its expert by the prefix of tiles, then N-tile, M-tile
-// (M fastest, so that an expert's tiles meet its weights in the L2 together).
+// Tile t of the kind in expert e, whose tiles are t0 .. t1 and rows r0 .. r1:
+// N-tile, then M-tile (M fastest, so that an expert's tiles meet its weights in
+// the L2 together).
+template <int MODE, int KIND>
+__device__ __forceinline__ void place(const Gemm& g, int t, int e, int t0, int t1, int r0, int r1, Unit& u)
+{
+    const int mts = t1 - t0, local = t - t0 * g.ntn;
+    const int nt = local / mts, v0 = local % mts * mx_rows(KIND);
+    u.e = uni(e);
+    u.n0 = uni(nt * (MODE == kGateUp ? kTN / 2 : kTN));
+    u.rows = uni(min(mx_rows(KIND), r1 - r0 - v0));
+    u.x0 = uni(r0 + v0);
+}
+
+// The tile's expert by the prefix of tiles: scalar loads, which do not wait
+// for the copies in flight.
 template <int MODE, int KIND>
 __device__ __forceinline__ void tile_of(const Gemm& g, int t, Unit& u)
 {
@@ -353,17 +391,43 @@ __device__ __forceinline__ void tile_of(const Gemm& g, int t, Unit& u)
         if (ldc(ts, mid) * g.ntn <= t) lo = mid;
         else hi = mid - 1;
     }
-    const int first = ldc(ts, lo), mts = ldc(ts, lo + 1) - first;
-    const int local = t - first * g.ntn;
-    const int r0 = ldc(rs, lo), c = ldc(rs, lo + 1) - r0;
-    const int nt = local / mts, v0 = local % mts * mx_rows(KIND);
-    u.e = uni(lo);
-    u.n0 = uni(nt * (MODE == kGateUp ? kTN / 2 : kTN));
-    u.rows = uni(min(mx_rows(KIND), c - v0));
-    u.x0 = uni(r0 + v0);
+    place<MODE, KIND>(g, t, lo, ldc(ts, lo), ldc(ts, lo + 1), ldc(rs, lo), ldc(rs, lo + 1), u);
 }
 
+// The same by one round of loads over the wave, where nothing else is in
+// flight yet (a launch's first units, the fixup): the search's dependent loads,
+// cold after the schedule kernel, were about 4 us of every launch.
 template <int MODE, int KIND>
+__device__ __forceinline__ void tile_by_wave(const Gemm& g, int t, Unit& u)
+{
+    const int32_t* ts = g.sched + KIND * (g.E + 1);
+    const int32_t* rs = g.sched + kMxKinds * (g.E + 1);
+    const int lane = threadIdx.x & 63;
+    int a[4], b[4], c[4], d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = min(64 * i + lane, g.E - 1);
+        a[i] = ts[e];
+        b[i] = ts[e + 1];
+        c[i] = rs[e];
+        d[i] = rs[e + 1];
+    }
+    int chunk = 0, at = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const uint64_t hit = __ballot(a[i] * g.ntn <= t && t < b[i] * g.ntn);
+        if (hit) {
+            chunk = i;
+            at = __builtin_ctzll(hit);
+        }
+    }
+    auto of = [&](const int* v) {
+        return __builtin_amdgcn_readlane(chunk == 0 ? v[0] : chunk == 1 ? v[1] : chunk == 2 ? v[2] : v[3], at);
+    };
+    place<MODE, KIND>(g, t, 64 * chunk + at, of(a), of(b), of(c), of(d), u);
+}
+
+template <int MODE, int KIND, bool WAVE = false>
 __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
 {
     Unit u;
@@ -378,7 +442,8 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
         u.KT = uni((p + 1) * KT / w.S) - u.k0;
         t = w.full + uni(u.pidx % w.L);
     }
-    tile_of<MODE, KIND>(g, t, u);
+    if (WAVE) tile_by_wave<MODE, KIND>(g, t, u);
+    else tile_of<MODE, KIND>(g, t, u);
     // Rows a multiple of 4 KB apart: if every workgroup walked K from the same
     // stage, the lines in flight would share their low address bits and crowd
     // a few memory channels, so neighbouring N-tiles start four stages apart
@@ -621,11 +686,11 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // what the previous kind left in flight has landed, in every wave
     wait_vm_lgkm<0>();
     slot_barrier();
-    Unit u = unit_of<MODE, KIND>(g, work, j), un = u;
+    Unit u = unit_of<MODE, KIND, true>(g, work, j), un = u;
     copy_list<KIND>(g, u, list_u(0), wave, lane);
     bool more = j + g.P < end;
     if (more) {
-        un = unit_of<MODE, KIND>(g, work, j + g.P);
+        un = unit_of<MODE, KIND, true>(g, work, j + g.P);
         copy_list<KIND>(g, un, list_u(1), wave, lane);
     }
     wait_vm_lgkm<0>();
@@ -833,11 +898,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     auto list = [&](int m) { return reinterpret_cast<const int32_t*>(lds + GE::kList0 + m % 3 * GE::kRows * 4); };
     auto list_u = [&](int m) { return lds_u + GE::kList0 + m % 3 * GE::kRows * 4; };
 
-    Unit u = unit_of<MODE, 0>(g, work, j), un = u;
+    Unit u = unit_of<MODE, 0, true>(g, work, j), un = u;
     copy_list<0>(g, u, list_u(0), wave, lane);
     bool more = unit_at(1) < end;
     if (more) {
-        un = unit_of<MODE, 0>(g, work, unit_at(1));
+        un = unit_of<MODE, 0, true>(g, work, unit_at(1));
         copy_list<0>(g, un, list_u(1), wave, lane);
     }
     wait_vm_lgkm<0>();
@@ -1091,7 +1156,7 @@ __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
     const int t = item / GE::TB, i = item % GE::TB;
     if (w.S == 1 || t >= w.L) return;
     Unit u;
-    tile_of<MODE, KIND>(g, w.full + t, u);
+    tile_by_wave<MODE, KIND>(g, w.full + t, u);
     const int wave = uni((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / GE::WN;
     if ((i * GE::WM + wm) * 32 >= u.rows) return;
