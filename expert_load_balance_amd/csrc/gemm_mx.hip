@@ -49,6 +49,7 @@ constexpr int kTK = moe::kMxStage;
 constexpr int kWBytes = kTN * kTK;       // 32 KB of weights per stage
 constexpr int kWCopies = kWBytes / 4096; // 16-byte copies per wave per stage
 constexpr int kSplitRounds = 3;
+constexpr int kNothing = 0x7fffffff;     // stages of the stream past the last unit
 constexpr int kPieces = 4;               // of an expert, loaded ahead of their number
 enum { kGateUp = 0, kDown = 1 };
 
@@ -165,19 +166,19 @@ __device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t range)
     i32x4 r;
     r[0] = uni((int32_t)(uint32_t)b);
     r[1] = uni((int32_t)(uint32_t)(b >> 32));  // stride 0, no swizzle
-    r[2] = uni((int32_t)range);
+    r[2] = (int32_t)range;
     r[3] = 0x00020000;                         // data format 32
     return r;
 }
 __device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(uni(soff)), "s"(uni((int)lds)) : "memory", "m0");
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(uni(soff)), "s"(uni((int)lds)) : "memory", "m0");
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -307,6 +308,17 @@ __device__ __forceinline__ int opaque_v(int v)
     return r;
 }
 
+// A constant in a scalar register of its own: where a value per lane needs the
+// same constant, the compiler would take both from one vector register, and
+// all that follows from the scalar one with it.
+template <int V>
+__device__ __forceinline__ int scalar()
+{
+    int r;
+    asm volatile("s_mov_b32 %0, %1" : "=s"(r) : "i"(V));
+    return r;
+}
+
 // ------------------------------------------------------------ work units --
 
 // Units of one kind: `full` whole tiles, then L leftover tiles in S K-parts
@@ -345,6 +357,22 @@ struct Gemm {
     uint16_t* y;
     float* part[kMxKinds];
 };
+
+// The launch's arguments (the kernel's first argument is a Gemm), read again
+// where this stands: they serve between tiles only, and held across a tile's
+// stages they would push the addresses that the stages need out of the scalar
+// registers.
+__device__ __forceinline__ Gemm again()
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    typedef const __attribute__((address_space(4))) Gemm constant;
+    constant* p = (constant*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *p;
+#else
+    return Gemm{};
+#endif
+}
 
 // The units of kinds 0 .. KIND - 1 come first.
 template <int MODE>
@@ -475,18 +503,19 @@ struct Geo {
     static constexpr int kACopies = kRows / 32;              // per wave per stage
     static constexpr int kPerStage = kWCopies + kACopies + 2;
     // LDS, kinds 1..3: slots of rows + weights, then their scales, then three
-    // row lists. Kind 0: two slots of rows, a ring of 21 weight units of 32
-    // rows (a stage takes 8), the scales of up to four stages (16 bytes for
+    // row lists. Kind 0: two slots of rows, a ring of 5 weight units of 128
+    // rows (a stage takes two), the scales of up to four stages (16 bytes for
     // each weight row, then for each row), the lists.
     static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
     static constexpr int kScale = (kTN + kRows) * (KIND == 0 ? 16 : 4);
     static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > 4
                                                       ? 4 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
     static constexpr int kAhead = KIND == 0 ? 2 : kSlots - 1;  // stages copied ahead of the products
-    static constexpr int kUnits = KIND == 0 ? 21 : 0, kUnit0 = kSlots * kSlot;
-    static constexpr int kScale0 = kUnit0 + kUnits * 4096;
+    static constexpr int kUnits = KIND == 0 ? 5 : 0, kUnit0 = kSlots * kSlot;
+    static constexpr int kScale0 = kUnit0 + kUnits * 16384;
     static constexpr int kList0 = kScale0 + (KIND == 0 ? 1 : kSlots) * kScale;
-    static constexpr int kBytes = kList0 + 3 * kRows * 4;
+    static constexpr int kKept0 = kList0 + 3 * kRows * 4;      // kind 0: three units for each wave
+    static constexpr int kBytes = kKept0 + (KIND == 0 ? 4 * 3 * 32 : 0);
     // Stages of a unit in the stream: at least kAhead, so that the copies are
     // never more than one unit ahead.
     __device__ static int stream_stages(int KT) { return KT < kAhead ? kAhead : KT; }
@@ -521,10 +550,10 @@ constexpr int kLds = max4(Geo<kGateUp, 0>::kBytes, Geo<kGateUp, 1>::kBytes, Geo<
 template <int MODE, int KIND>
 struct Copier {
     using GE = Geo<MODE, KIND>;
-    const char *ab, *asb, *wb0, *wb1, *sb;
+    const char *ab, *wb0, *wb1, *asb, *sb;  // rows, weight blocks 0..3 and 4..7, scales
+    int upper;                              // down: weight rows from block 4 on (0 or less: none)
     uint32_t aoff[GE::kACopies], woff, asoff, wsoff;
     int rows32;        // bytes of 32 weight rows
-    bool upper;        // weight blocks 4..7 lie inside the matrix
     int rot;
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
 
@@ -534,41 +563,54 @@ struct Copier {
         const int K = MODE == kGateUp ? g.H : g.F, KS = K / moe::kMxBlock, wrows = MODE == kGateUp ? g.F : g.H;
         const size_t e0 = (size_t)u.e * wrows;
         const size_t x0 = MODE == kGateUp ? 0 : (size_t)u.x0;
+        // (in the down projection's last tile weight blocks 4..7 may lie past
+        // the matrix)
+        upper = wrows - u.n0 - kTN / 2;
         ab = uni_ptr((const char*)g.a + x0 * K + u.k0 * kTK);
-        asb = uni_ptr((const char*)g.as + x0 * KS + u.k0 * 4);
         wb0 = uni_ptr((const char*)g.w0 + e0 * K + u.k0 * kTK);
-        wb1 = MODE == kGateUp ? uni_ptr((const char*)g.w1 + e0 * K + u.k0 * kTK) : wb0;
+        wb1 = uni_ptr((const char*)(MODE == kGateUp ? g.w1 : g.w0) + e0 * K + u.k0 * kTK);
+        asb = uni_ptr((const char*)g.as + x0 * KS + u.k0 * 4);
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + u.k0 * 4);
-        st = 0;
+        st = scalar<0>();
         rot = u.rot;
         real = u.KT;
         KT = GE::stream_stages(u.KT);
-        auto source = [&](int r) { return MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r; };
+        // (looked up for padding rows too: as a load under a condition it would be
+        // a branch, and what is set beside it a value per lane)
+        auto source = [&](int r) {
+            uint32_t x = MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r;
+            asm volatile("" : "+v"(x));
+            return x;
+        };
         auto weight = [&](int r) {
             return (uint32_t)(MODE == kGateUp ? u.n0 + (r & 127) : min(u.n0 + r, wrows - 1));
         };
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) {
             const int r = 8 * (wave + 4 * i) + (lane >> 3);
-            aoff[i] = r < u.rows ? source(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16) : kZeroRow;
+            const uint32_t off = source(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16);
+            aoff[i] = r < u.rows ? off : kZeroRow;
         }
-        // (blocks of 32 weight rows are 32 K bytes apart; in the down
-        // projection's last tile the upper four may lie past the matrix)
+        // (blocks of 32 weight rows are 32 K bytes apart)
         const int r0 = 8 * wave + (lane >> 3);
         woff = (uint32_t)(u.n0 + r0) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r0)) * 16);
         rows32 = 32 * K;
-        upper = MODE == kGateUp || u.n0 + kTN / 2 < wrows;
-        const int ar = GE::kRows / 4 * wave + lane;
-        asoff = lane < GE::kRows / 4 && ar < u.rows ? source(ar) * (uint32_t)KS : kZeroRow;
+        const int ar = GE::kRows / 4 * wave + lane % (GE::kRows / 4);
+        const uint32_t aso = source(ar) * (uint32_t)KS;
+        asoff = lane < GE::kRows / 4 && ar < u.rows ? aso : kZeroRow;
         wsoff = weight(64 * wave + lane) * (uint32_t)KS;
     }
     __device__ __forceinline__ void nothing()
     {
-        st = real = rot = 0;
-        KT = 0x7fffffff;
+        st = real = rot = scalar<0>();
+        KT = kNothing;
     }
     __device__ __forceinline__ int ks() const { return st + rot >= real ? st + rot - real : st + rot; }
-    __device__ __forceinline__ uint32_t range() const { return st < real ? kCopyRange : 0u; }
+    // A stage past the unit's last is a copy of nothing (a unit of kind 0 has at
+    // least four stages, so only the last unit has such). As a comparison of a
+    // scalar where it is used: a range that came round the loop would be kept
+    // in a vector register.
+    __device__ __forceinline__ uint32_t range() const { return (KIND == 0 ? KT != kNothing : st < real) ? kCopyRange : 0u; }
     // The next stage into a slot; each call of row and weight is one
     // instruction, scales is two.
     __device__ __forceinline__ void row(int i, uint32_t slot, int wave) const
@@ -577,7 +619,7 @@ struct Copier {
     }
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
-        copy16(buffer_of(i < 4 ? wb0 : wb1, i < 4 || upper ? range() : 0u), woff,
+        copy16(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
                ks() * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
@@ -678,7 +720,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // tiles, bound by the products, they would double the time.
     constexpr bool kWide = MODE == kGateUp && KIND >= 2;
     const KindWork work = work_of<MODE>(g, KIND);
-    const int end = work.first + work.count;
+    const int end = work.first + work.count, P = g.P;
     // this workgroup's first unit of the kind
     int j = work.first + uni((slot_id - work.first % g.P + g.P) % g.P);
     if (j >= end) return;
@@ -708,7 +750,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     int to = 0;      // slot of the next copies
     auto copy_next = [&]() {
         if (cp.st == cp.KT) {
-            if (more) cp.setup(g, un, list(m + 1), wave, opaque_v(lane));
+            if (more) cp.setup(again(), un, list(m + 1), wave, opaque_v(lane));
             else cp.nothing();
         }
         cp.stage(lds_u + (uint32_t)to * GE::kSlot, lds_u + GE::kScale0 + (uint32_t)to * GE::kScale, wave, lane);
@@ -738,10 +780,11 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                 // of the unit before this one, whose epilogue is done; it
                 // lands before the first stage of the next unit does, whose
                 // copies follow it
-                more2 = j + 2 * g.P < end;
+                more2 = j + 2 * P < end;
                 if (more2) {
-                    u2 = unit_of<MODE, KIND>(g, work, j + 2 * g.P);
-                    copy_list<KIND>(g, u2, list_u(m + 2), wave, lane);
+                    const Gemm ga = again();
+                    u2 = unit_of<MODE, KIND>(ga, work, j + 2 * P);
+                    copy_list<KIND>(ga, u2, list_u(m + 2), wave, lane);
                 }
             }
             copy_next();
@@ -804,64 +847,82 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
             }
         }
         drain();
+        const Gemm ga = again();
         if (u.pidx >= 0) {
 #pragma unroll
-            for (int b = 0; b < GE::TB; ++b) store_part<MODE, KIND>(g, u, b, acc[b], wave, opaque_v(lane));
+            for (int b = 0; b < GE::TB; ++b) store_part<MODE, KIND>(ga, u, b, acc[b], wave, opaque_v(lane));
         } else {
 #pragma unroll
-            for (int b = 0; b < GE::TB; ++b) finish<MODE, KIND>(g, u, b, acc[b], list(m), wave, opaque_v(lane));
+            for (int b = 0; b < GE::TB; ++b) finish<MODE, KIND>(ga, u, b, acc[b], list(m), wave, opaque_v(lane));
         }
         if (!more) break;
         u = un;
         un = u2;
         more = more2;
-        j += g.P;
+        j += P;
         ++m;
     }
 }
 
 // ------------------------------------------------------- 256-row tiles --
-// A stage is 32 MFMAs of 64 cycles a wave on 66 KB of copies, and a CU's
-// copies run at about 55 GB/s (26 bytes a cycle), so the two are near each
-// other and have to overlap throughout. All copies of a stage in one of its
-// halves took 2.5 us a stage: the waves that issue them wait for the copy
-// path and their MFMAs with them. So each half issues its part:
+// A stage is 32 MFMAs of 64 cycles a wave on 64 KB of copies and 128 KB of LDS
+// reads, so the three have to overlap throughout:
 //   first half of stage s: the products of its first 64 values of K, the reads
-//     of the second 64, and the copies of weight units 0..4 of stage s + 2,
-//     into the five units of the ring that no stage in use holds;
+//     of the second 64, and the copies of the first 128 weight rows of stage
+//     s + 2, into the fifth unit of the ring, which no stage in use holds;
 //   one barrier: stage s's fragments are all in registers (its units and its
 //     row slot are free) and stage s + 1 has landed (each wave waits for its
-//     own copies but the five it just issued);
-//   second half: the other products, the copies of units 5..7 and of the rows
-//     of stage s + 2, and the reads of stage s + 1's first 64 values.
-// A copy of scales touches a line per lane and so takes the copy path as long
-// as a kilobyte of weights; 4 bytes a stage for each of the 512 rows cost 16 %
-// of the time. They come in groups of up to four stages instead (16 bytes a
-// row): a group waits in LDS, is read into registers in the last stage of the
-// group before it, and its place is filled again in the stage after.
+//     own copies but the four it just issued);
+//   second half: the other products, the copies of the other weight rows and of
+//     the rows of stage s + 2, and the reads of stage s + 1's first 64 values.
+// (All copies in one half took 2.5 us a stage: the waves that issue them wait
+// for the copy path, and their MFMAs with them.)
+//
+// Measured on random codes: 1.9 to 2.1 us a stage whether the weights come from
+// HBM or from the L2, the matrix pipes busy 62 to 75 % of the cycles at a clock
+// of 1.3 to 1.65 GHz. The chip's power is the bound: taking the ring's address
+// arithmetic out of the loop (units of 32 rows before, 270 instructions beside
+// the products, now 192) cut 3020 cycles a stage to 2730 and the clock from
+// 1.50 to 1.31 GHz with them; 8 experts of 512 rows of 4096 x 14336 went from
+// 519 to 484 us (gate/up, 1.99 PFLOP/s) and from 245 to 232 us (down).
+//
+// One wave's vector memory instruction costs as much for 64 lines of 16 bytes as
+// for a kilobyte in 8: copies of 4 bytes of scales a stage for each of the 512
+// rows cost 16 % of the time. They come in groups of up to four stages instead
+// (16 bytes a row): a group waits in LDS, is read into registers in the last
+// stage of the group before it, and its place is filled again in the stage
+// after.
+
+// The product of a half stage after which fragment id (0..3 weights, 4..7 rows)
+// of the other half is read: the weights first, a row block once the same
+// block of this half has been used (it can take its registers), the last ones
+// early enough to arrive before the half ends.
+__host__ __device__ constexpr int read_at(int id, int products)
+{
+    return id < 4 ? (id < products ? id : products - 1)
+                  : 4 * (id - 3) < products - 3 ? 4 * (id - 3) : products - 3;
+}
 
 // Groups of scales of a workgroup's units of kind 0, in the order of the
 // stream: stages a .. a + len of K, loaded from stage a - skip on (the last 16
 // bytes of a row, near its end). No group but a whole unit has one stage.
 template <int MODE>
 struct ScaleStream {
-    const char *asb, *sb;
     uint32_t asoff;
-    int n0, wrows, KS, at, left, KT_all, len, skip;
+    int e, n0, x0, at, left, len, skip;
 
     __device__ __forceinline__ void setup(const Gemm& g, const Unit& u, const int32_t* list, int wave, int lane)
     {
-        const int K = MODE == kGateUp ? g.H : g.F;
-        KS = K / moe::kMxBlock;
-        wrows = MODE == kGateUp ? g.F : g.H;
+        const int KS = (MODE == kGateUp ? g.H : g.F) / moe::kMxBlock;
+        e = u.e;
         n0 = u.n0;
-        asb = uni_ptr((const char*)g.as + (MODE == kGateUp ? 0 : (size_t)u.x0 * KS));
-        sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + (size_t)u.e * wrows * KS);
+        x0 = MODE == kGateUp ? 0 : u.x0;
         at = u.k0 + u.rot;
         left = Geo<MODE, 0>::stream_stages(u.KT);
-        KT_all = K / kTK;
         const int r = 64 * wave + lane;
-        asoff = r < u.rows ? (MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r) * (uint32_t)KS : kZeroRow;
+        uint32_t off = (MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r) * (uint32_t)KS;
+        asm volatile("" : "+v"(off));  // (as in Copier)
+        asoff = r < u.rows ? off : kZeroRow;
     }
     __device__ __forceinline__ void nothing()  // the last unit's scales again, for no one
     {
@@ -869,16 +930,18 @@ struct ScaleStream {
         left = 0x7fffffff;
     }
     // copies the next group
-    __device__ __forceinline__ void copy(uint32_t lds, int wave, int lane)
+    __device__ __forceinline__ void copy(const Gemm& g, uint32_t lds, int wave, int lane)
     {
-        const int r = 64 * wave + lane;
-        const uint32_t wsoff = (uint32_t)(MODE == kGateUp ? n0 + (r & 127) : min(n0 + r, wrows - 1)) * (uint32_t)KS;
-        const int from = min(at, KT_all - 4);
+        const int K = MODE == kGateUp ? g.H : g.F, KS = K / moe::kMxBlock, wrows = MODE == kGateUp ? g.F : g.H;
+        const int KT_all = K / kTK, from = min(at, KT_all - 4);
         skip = at - from;
         len = min(4 - skip, left);
         if (left - len == 1 && len > 1) --len;
-        copy16(buffer_of(sb, kCopyRange), wsoff, from * 4, lds + wave * 1024);
-        copy16(buffer_of(asb, kCopyRange), asoff, from * 4, lds + kTN * 16 + wave * 1024);
+        const int r = 64 * wave + lane;
+        const uint32_t wsoff = (uint32_t)(MODE == kGateUp ? n0 + (r & 127) : min(n0 + r, wrows - 1)) * (uint32_t)KS;
+        const uint8_t* s = MODE == kGateUp && wave >= 2 ? g.s1 : g.s0;
+        copy16(buffer_of(s + (size_t)e * wrows * KS, kCopyRange), wsoff, from * 4, lds + wave * 1024);
+        copy16(buffer_of(g.as + (size_t)x0 * KS, kCopyRange), asoff, from * 4, lds + kTN * 16 + wave * 1024);
         at += len;
         if (at == KT_all) at = 0;  // (only where the unit began past 0)
         left -= len;
@@ -886,7 +949,7 @@ struct ScaleStream {
 };
 
 template <int MODE>
-__device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
+__device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
 {
     using GE = Geo<MODE, 0>;
     const KindWork work = work_of<MODE>(g, 0);
@@ -894,9 +957,12 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     // Round r's tile at position p goes to slot p + r: tails lie between whole
     // tiles at regular distances, and no slot should get only the one or the
     // other.
-    auto unit_at = [&](int r) { return r * g.P + uni((slot_id - r % g.P + g.P) % g.P); };
-    const int j = unit_at(0);
-    if (j >= end) return;
+    auto unit_at = [](const Gemm& g, int r) {
+        const int b = blockIdx.x, slot = b % 8 * (g.P / 8) + b / 8;
+        return r * g.P + uni((slot - r % g.P + g.P) % g.P);
+    };
+    const int units = uni(end / g.P + (unit_at(g, end / g.P) < end));  // this workgroup's
+    if (units == 0) return;
 
     const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
     const int fr = lane & 31, half = lane >> 5, wm = wave >> 1, wn = wave & 1;
@@ -904,11 +970,23 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     auto list = [&](int m) { return reinterpret_cast<const int32_t*>(lds + GE::kList0 + m % 3 * GE::kRows * 4); };
     auto list_u = [&](int m) { return lds_u + GE::kList0 + m % 3 * GE::kRows * 4; };
 
-    Unit u = unit_of<MODE, 0, true>(g, work, j), un = u;
+    // the units ahead wait in LDS, each wave's own copies: scalar registers held
+    // across a tile's stages would be spilled
+    auto keep = [&](int m, const Unit& u) {
+        int4* p = reinterpret_cast<int4*>(lds + GE::kKept0) + (wave * 3 + m % 3) * 2;
+        p[0] = make_int4(u.e, u.n0, u.rows, u.x0);
+        p[1] = make_int4(u.k0, u.KT, u.pidx, u.rot);
+    };
+    auto kept = [&](int m) {
+        const int4* p = reinterpret_cast<const int4*>(lds + GE::kKept0) + (wave * 3 + m % 3) * 2;
+        const int4 a = p[0], b = p[1];
+        return Unit{uni(a.x), uni(a.y), uni(a.z), uni(a.w), uni(b.x), uni(b.y), uni(b.z), uni(b.w)};
+    };
+    Unit u = unit_of<MODE, 0, true>(g, work, unit_at(g, 0));
     copy_list<0>(g, u, list_u(0), wave, lane);
-    bool more = unit_at(1) < end;
-    if (more) {
-        un = unit_of<MODE, 0, true>(g, work, unit_at(1));
+    if (units > 1) {
+        const Unit un = unit_of<MODE, 0, true>(g, work, unit_at(g, 1));
+        keep(1, un);
         copy_list<0>(g, un, list_u(1), wave, lane);
     }
     wait_vm_lgkm<0>();
@@ -916,20 +994,20 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     Copier<MODE, 0> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0, odd = 0;  // this unit's number; parity of the stage being computed
-    constexpr int kEarly = GE::kUnits - 16;  // weight units copied in a stage's first half
+    constexpr int kEarly = 4;  // weight copies in a stage's first half (one unit)
     // the copies move on to the next unit
     auto follow = [&]() {
         if (cp.st == cp.KT) {
-            if (more) cp.setup(g, un, list(m + 1), wave, opaque_v(lane));
+            if (m + 1 < units) cp.setup(again(), kept(m + 1), list(m + 1), wave, opaque_v(lane));
             else cp.nothing();
         }
     };
     auto slot_u = [&](int n) { return lds_u + (uint32_t)n * GE::kSlot; };
-    // ring units: first unit of the stage being computed, of the next, and of
-    // the one being copied
+    // ring units: the stage being computed holds units wat and wat + 1, the
+    // next one the two after them, and so on
     auto wrap = [&](int x) { return x >= GE::kUnits ? x - GE::kUnits : x; };
     int wat = 0;
-    auto unit_u = [&](int first, int i) { return lds_u + GE::kUnit0 + (uint32_t)wrap(first + i) * 4096u; };
+    auto unit_u = [&](int unit, int i) { return lds_u + GE::kUnit0 + (uint32_t)unit * 16384u + (uint32_t)(i % 4) * 4096u; };
 
     i32x8 wf[2][4], tf[2][4];
     // Scales of this stage and the rest of its group: the lane's two bytes of
@@ -940,14 +1018,18 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     // lane's four chunks (half, half + 2, + 4, + 6) the others differ from
     // the first in address bits 5 and 6
     const uint32_t fc = (uint32_t)((half ^ swz(fr)) * 16);
-    const uint32_t wfa = (uint32_t)(GE::kUnit0 + fr * 128) + fc;
+    const uint32_t wfa = (uint32_t)(GE::kUnit0 + (MODE == kGateUp ? wn * 64 : 0) * 128 + fr * 128) + fc;
     const uint32_t tfa = (uint32_t)((wm * 32 + fr) * 128) + fc;
     // fragment id (0..3 weights, 4..7 rows) of the stage in row slot n whose
     // weights start at unit w0 of the ring
     auto read = [&](int n, int w0, int kk, int id) {
         if (id < 4) {
-            const uint32_t at = (wfa ^ (uint32_t)(64 * kk)) + (uint32_t)wrap(w0 + GE::wrow(wn, id) / 32) * 4096u;
-            wf[kk][id] = frag(lds + at, lds + (at ^ 32u));
+            // gate/up: blocks 0, 1 in the stage's first unit (gate), 2, 3 in the
+            // second; down: all four in unit wn
+            const int unit = MODE == kGateUp ? (id < 2 ? w0 : wrap(w0 + 1)) : wn == 0 ? w0 : wrap(w0 + 1);
+            const int o = MODE == kGateUp ? (id % 2) * 4096 : id * 4096;
+            const uint32_t at = (wfa ^ (uint32_t)(64 * kk)) + (uint32_t)unit * 16384u;
+            wf[kk][id] = frag(lds + at + o, lds + (at ^ 32u) + o);
         } else {
             const uint32_t at = (tfa ^ (uint32_t)(64 * kk)) + (uint32_t)n * GE::kSlot;
             const int o = (id - 4) * 8192;
@@ -990,19 +1072,19 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     ScaleStream<MODE> sc;
     auto copy_group = [&](int lists) {
         if (sc.left == 0) {
-            if (more) sc.setup(g, un, list(lists + 1), wave, opaque_v(lane));
+            if (lists + 1 < units) sc.setup(again(), kept(lists + 1), list(lists + 1), wave, opaque_v(lane));
             else sc.nothing();
         }
-        sc.copy(lds_u + GE::kScale0, wave, opaque_v(lane));
+        sc.copy(again(), lds_u + GE::kScale0, wave, opaque_v(lane));
     };
     sc.setup(g, u, list(0), wave, lane);
-    sc.copy(lds_u + GE::kScale0, wave, opaque_v(lane));
+    sc.copy(again(), lds_u + GE::kScale0, wave, opaque_v(lane));
     int glen = sc.len;         // stages of this group that are left
     const int gskip = sc.skip;
     for (int n = 0; n < 2; ++n) {
         follow();
 #pragma unroll
-        for (int i = 0; i < kWCopies; ++i) cp.weight(i, unit_u(8 * n, i), wave);
+        for (int i = 0; i < kWCopies; ++i) cp.weight(i, unit_u(2 * n + i / 4, i), wave);
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) cp.row(i, slot_u(n), wave);
         ++cp.st;
@@ -1018,13 +1100,10 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
     int nlen = sc.len, nskip = sc.skip;  // the group in LDS
     bool refill = false;                 // it has been read: its place is free
 
-    Unit u2 = un;
-    bool more2 = false;
     // One unit whose rows fill NB token blocks of each wave (32 rows of every
     // 64): its stages and its epilogue.
     auto run = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value, kM = 4 * NB;  // products per half stage
-        constexpr int kSpread = NB > 2 ? 8 : kM;  // products over which a half's reads are spread
         f32x16 acc[NB][4];
 #pragma unroll
         for (int i = 0; i < NB; ++i)
@@ -1040,11 +1119,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
                 // the unit after next: its list goes to the place of the list
                 // of the unit before this one, whose epilogue every wave left
                 // before stage 0's barrier
-                const int j2 = unit_at(m + 2);
-                more2 = j2 < end;
-                if (more2) {
-                    u2 = unit_of<MODE, 0>(g, work, j2);
-                    copy_list<0>(g, u2, list_u(m + 2), wave, lane);
+                if (m + 2 < units) {
+                    const Gemm ga = again();
+                    const Unit u2 = unit_of<MODE, 0>(ga, work_of<MODE>(ga, 0), unit_at(ga, m + 2));
+                    keep(m + 2, u2);
+                    copy_list<0>(ga, u2, list_u(m + 2), wave, opaque_v(lane));
                 }
             }
             follow();
@@ -1061,13 +1140,14 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             if (refill) {  // the next stage starts the group in LDS
                 read_group(wsn, tsn, nskip);
             }
-            const int wnext = wrap(wat + 8), wcopy = wrap(wnext + 8);
+            const int wnext = wrap(wat + 2), wcopy = wrap(wnext + 2), wcopy1 = wrap(wcopy + 1);
 #pragma unroll
             for (int q = 0; q < kM; ++q) {
                 acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
                 // this half's share of the reads (NB row blocks) and copies
 #pragma unroll
-                for (int z = q * 8 / kSpread; z < (q + 1) * 8 / kSpread && z < 4 + NB; ++z) read(odd, wat, 1, z);
+                for (int z = 0; z < 4 + NB; ++z)
+                    if (read_at(z, kM) == q) read(odd, wat, 1, z);
 #pragma unroll
                 for (int z = q * kEarly / kM; z < (q + 1) * kEarly / kM; ++z) cp.weight(z, unit_u(wcopy, z), wave);
                 __builtin_amdgcn_sched_barrier(0);
@@ -1082,10 +1162,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
                 for (int z = q * 12 / kM; z < (q + 1) * 12 / kM; ++z) {
                     if (z < GE::kACopies) cp.row(z, sl, wave);
                     else if (z - GE::kACopies < kWCopies - kEarly)
-                        cp.weight(kEarly + z - GE::kACopies, unit_u(wcopy, kEarly + z - GE::kACopies), wave);
+                        cp.weight(kEarly + z - GE::kACopies, unit_u(wcopy1, z), wave);
                 }
 #pragma unroll
-                for (int z = q * 8 / kSpread; z < (q + 1) * 8 / kSpread && z < 8; ++z) read(odd ^ 1, wnext, 0, z);
+                for (int z = 0; z < 8; ++z)
+                    if (read_at(z, kM) == q) read(odd ^ 1, wnext, 0, z);
                 // scales that no product of this stage needs any more
                 if (q % 4 == 3 && q < kM - 1) next_scale(ts[q >> 2], tsn[q >> 2], refill);
                 if (q >= kM - 4) next_scale(ws[q - (kM - 4)], wsn[q - (kM - 4)], refill);
@@ -1100,13 +1181,14 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
             glen = refill ? nlen : glen - 1;
         }
         drain();
+        const Gemm ga = again();
         if (u.pidx >= 0) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) store_part<MODE, 0>(g, u, i, acc[i], wave, opaque_v(lane));
+            for (int i = 0; i < NB; ++i) store_part<MODE, 0>(ga, u, i, acc[i], wave, opaque_v(lane));
         } else {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                finish<MODE, 0>(g, u, i, acc[i], list(m), wave, opaque_v(lane));
+                finish<MODE, 0>(ga, u, i, acc[i], list(m), wave, opaque_v(lane));
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -1116,11 +1198,8 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds, int slot_id)
         else if (u.rows > 128) run(std::integral_constant<int, 3>{});
         else if (u.rows > 64) run(std::integral_constant<int, 2>{});
         else run(std::integral_constant<int, 1>{});
-        if (!more) break;
-        u = un;
-        un = u2;
-        more = more2;
-        ++m;
+        if (++m == units) break;
+        u = kept(m);
     }
 }
 
@@ -1130,7 +1209,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const int b = blockIdx.x;
     const int slot_id = b % 8 * (g.P / 8) + b / 8;
-    big_tiles<MODE>(g, lds, slot_id);
+    big_tiles<MODE>(g, lds);
     ring_tiles<MODE, 1>(g, lds, slot_id);
     ring_tiles<MODE, 2>(g, lds, slot_id);
     ring_tiles<MODE, 3>(g, lds, slot_id);
