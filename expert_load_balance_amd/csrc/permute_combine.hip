@@ -151,7 +151,8 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(int T, int k, int E, 
 
 // The 8-bit dispatch: as permute_kernel on rows of H code bytes; the
 // wavefront of a row's first chunk also moves its H / 32 scale bytes (whole
-// dwords: H % 128 == 0).
+// dwords: H % 128 == 0). Bound by the writes: 8192 tokens of 7168 to 8 rows
+// each, 94 us (0.54 GB, 5.8 TB/s).
 __global__ __launch_bounds__(kThreads) void permute_mx_kernel(int T, int k, int E, int R, int row_vecs,
                                                               int nchunks, int scale_words,
                                                               const uint4* __restrict__ q,
