@@ -180,10 +180,16 @@ __device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t range)
     r[3] = 0x00020000;                         // data format 32
     return r;
 }
+// STREAM: not kept in the caches (weights that no other workgroup reads).
+template <bool STREAM = false>
 __device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
+    if (STREAM)
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                     :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
 {
@@ -630,7 +636,11 @@ struct Copier {
     }
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
-        copy16(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
+        // An expert's one small tile reads its weights once: gate/up of 128 x 16
+        // rows of 4096 x 1536 279 -> 261 us, of 256 x 32 rows of 7168 x 2048 1404 ->
+        // 1320 us. 256-row tiles share theirs with the expert's other tiles
+        // (streamed, the 256-expert layer's gate/up took 2437 us for 2331).
+        copy16<KIND != 0>(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
                ks() * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
