@@ -39,6 +39,30 @@ __device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d,
 // as the magnitudes do, infinities above every number and NaN above those.
 __device__ __forceinline__ uint32_t mx_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// Calls that move more than the Infinity Cache holds (256 MB) read and write
+// past the caches (non-temporal): what they leave there serves no one, and the
+// dirty lines they push out cost bandwidth. Smaller ones leave their outputs for
+// the next kernel. Measured on a chain of a kernel that writes x, the norm, and
+// one that reads y, in us (kept / streamed), by the norm's bytes: forward 153 MB
+// 43 / 49, 229 MB 70 / 69, 305 MB 90 / 90, 534 MB 169 / 162; backward 46 / 48, 67 /
+// 68, 87 / 85, 170 / 152.
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint4* p)
+{
+    if (!STREAM) return *p;
+    const u32x4v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint4* p, const uint4& v)
+{
+    if (!STREAM) *p = v;
+    else __builtin_nontemporal_store(u32x4v{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4v*>(p));
+}
+
 // 8-bit GEMM geometry: a workgroup tile is 256, 128, 64 or 32 rows (kinds 0..3)
 // x 256 weight rows (gate/up: 128 of each), K in stages of 128 bytes (four
 // scale blocks), on at most kGemmMaxGrid persistent workgroups.

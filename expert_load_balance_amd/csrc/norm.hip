@@ -11,8 +11,9 @@
 // a CU and one row's loads cover another's sum.
 //
 // Measured: forward, 8192 rows of 7168 bf16 with residual, y and 8-bit output,
-// 96 us (5.5 TB/s; a plain copy of 2 GiB reaches 4.9, a read 6.2); backward of
-// the same, 91 us + 5 us for dweight's sum (4.9 TB/s); one row of 4096, 3 us.
+// 86 us (6.2 TB/s; a plain copy of 2 GiB reaches 4.9, a read 6.2), 96 us through
+// the caches; backward of the same, 82 us (91) + 5 us for dweight's sum (5.4
+// TB/s); one row of 4096, 3 us.
 #include <type_traits>
 
 #include "mx.h"
@@ -124,7 +125,7 @@ __device__ __forceinline__ void store_mx(const float* v, int64_t vec, bool in, u
 }
 
 // s, y may be x or residual: a thread stores a vector only after it read it
-template <bool BF16, int CH>
+template <bool BF16, int CH, bool STREAM>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, const uint4* x,
                                                               const uint4* residual,
                                                               const uint4* __restrict__ weight, float eps,
@@ -141,8 +142,8 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
         u[i] = make_uint4(0, 0, 0, 0);
         wv[i] = u[i];
         if (c < vecs) {
-            u[i] = x[base + c];
-            if (residual) r[i] = residual[base + c];
+            u[i] = moe::load16<STREAM>(x + base + c);
+            if (residual) r[i] = moe::load16<STREAM>(residual + base + c);
             wv[i] = weight[c];
         }
     }
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
         const int c = i * blockDim.x + threadIdx.x;
         if (residual && c < vecs) add_residual<BF16>(u[i], r[i], f[i]);
         else V::load(u[i], f[i]);
-        if (s && c < vecs) s[base + c] = u[i];
+        if (s && c < vecs) moe::store16<STREAM>(s + base + c, u[i]);
 #pragma unroll
         for (int k = 0; k < V::kN; ++k) ss = fma((double)f[i][k], (double)f[i][k], ss);
     }
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_kernel(int H, int vecs, c
         V::load(wv[i], w);
 #pragma unroll
         for (int k = 0; k < V::kN; ++k) f[i][k] = f[i][k] * rs * w[k];
-        if (y && c < vecs) y[base + c] = V::store(f[i]);
+        if (y && c < vecs) moe::store16<STREAM>(y + base + c, V::store(f[i]));
         if (q) store_mx<BF16>(f[i], base + c, c < vecs, q, scales);
     }
 }
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_wide_kernel(int H, int ve
 // Workgroup b takes rows b, b + G, ...; each thread keeps the fp32 sums of
 // its columns over those rows and writes them to part[b], so that the sum's
 // order is fixed.
-template <bool BF16, int CH, int TH>
+template <bool BF16, int CH, int TH, bool STREAM>
 __global__ __launch_bounds__(TH) void rmsnorm_bwd_kernel(int T, int H, int vecs, const uint4* s,
                                                                   const uint4* __restrict__ weight,
                                                                   const float* __restrict__ rstd,
@@ -254,9 +255,9 @@ __global__ __launch_bounds__(TH) void rmsnorm_bwd_kernel(int T, int H, int vecs,
             ud[i] = us[i];
             ue[i] = us[i];
             if (c < vecs) {
-                us[i] = s[base + c];
-                ud[i] = dy[base + c];
-                if (ds) ue[i] = ds[base + c];
+                us[i] = moe::load16<STREAM>(s + base + c);
+                ud[i] = moe::load16<STREAM>(dy + base + c);
+                if (ds) ue[i] = moe::load16<STREAM>(ds + base + c);
             }
         }
         float dot = 0.0f;
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(TH) void rmsnorm_bwd_kernel(int T, int H, int vecs,
 #pragma unroll
             for (int k = 0; k < V::kN; ++k)
                 e[k] = fmaf(rs, fmaf(-(a[k] * rs), mean, d[k] * w[k]), e[k]);
-            if (c < vecs) dx[base + c] = V::store(e);
+            if (c < vecs) moe::store16<STREAM>(dx + base + c, V::store(e));
         }
     }
 #pragma unroll
@@ -401,7 +402,7 @@ RowSplit row_split(int vecs)
     return ch <= kMaxCh ? RowSplit{t, ch} : RowSplit{kMaxThreads, 0};
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 hipError_t launch_norm(const moe_shape_t& sh, const void* x, const void* r, const void* w, float eps,
                        void* s, void* y, void* q, void* scales, float* rstd, hipStream_t st)
 {
@@ -414,8 +415,8 @@ hipError_t launch_norm(const moe_shape_t& sh, const void* x, const void* r, cons
     switch (p.ch) {
 #define MOE_NORM(C)                                                                                \
     case C:                                                                                        \
-        rmsnorm_kernel<BF16, C><<<sh.T, p.threads, 0, st>>>(sh.H, vecs, xv, rv, wv, eps, sv, yv, qv, \
-                                                            cv, rstd);                             \
+        rmsnorm_kernel<BF16, C, STREAM><<<sh.T, p.threads, 0, st>>>(sh.H, vecs, xv, rv, wv, eps, sv, \
+                                                                    yv, qv, cv, rstd);             \
         break;
         MOE_NORM(1) MOE_NORM(2) MOE_NORM(3) MOE_NORM(4)
 #undef MOE_NORM
@@ -429,7 +430,7 @@ hipError_t launch_norm(const moe_shape_t& sh, const void* x, const void* r, cons
 // The backward holds 7 vectors' worth of registers per vector of the row (s,
 // dy, ds, the weight and the fp32 sums), so it takes two vectors a thread on
 // up to 512 threads, then up to four.
-template <bool BF16>
+template <bool BF16, bool STREAM>
 hipError_t launch_norm_bwd(const moe_shape_t& sh, const void* s, const void* w, const float* rstd,
                            const void* dy, const void* ds, void* dx, float* part, int G, hipStream_t st)
 {
@@ -442,7 +443,7 @@ hipError_t launch_norm_bwd(const moe_shape_t& sh, const void* s, const void* w, 
     if (vecs > 4 * t) t = kMaxThreads;
     const int ch = (vecs + t - 1) / t;
 #define MOE_NORM(C, TH)                                                                              \
-    rmsnorm_bwd_kernel<BF16, C, TH><<<G, t, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev, xv, part)
+    rmsnorm_bwd_kernel<BF16, C, TH, STREAM><<<G, t, 0, st>>>(sh.T, sh.H, vecs, sv, wv, rstd, dv, ev, xv, part)
     if (t <= 512 && ch == 1) MOE_NORM(1, 512);
     else if (t <= 512 && ch == 2) MOE_NORM(2, 512);
     else if (t <= 512 && ch == 3) MOE_NORM(3, 512);
@@ -462,6 +463,10 @@ hipError_t moe_launch_rmsnorm(const moe_shape_t& s, const void* x, const void* r
                               const void* weight, float eps, void* s_out, void* y, void* q,
                               void* scales, float* rstd, hipStream_t st)
 {
+    const int64_t row = (int64_t)s.H * (s.dtype == MOE_BF16 ? 2 : 4);
+    const bool stream = s.T * (row * (1 + !!residual + !!s_out + !!y) + (q ? s.H : 0)) > moe::kStreamBytes;
+    auto* launch = s.dtype == MOE_BF16 ? (stream ? launch_norm<true, true> : launch_norm<true, false>)
+                                       : (stream ? launch_norm<false, true> : launch_norm<false, false>);
     // (past 2^32 threads a launch quietly runs the remainder only)
     moe_shape_t part = s;
     for (int64_t t0 = 0; t0 < s.T; t0 += kMaxRows) {
@@ -470,14 +475,8 @@ hipError_t moe_launch_rmsnorm(const moe_shape_t& s, const void* x, const void* r
             using Byte = std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(p)>>, const char, char>;
             return p ? static_cast<decltype(p)>(static_cast<Byte*>(p) + t0 * row_bytes) : nullptr;
         };
-        const int64_t row = (int64_t)s.H * (s.dtype == MOE_BF16 ? 2 : 4);
-        float* rs = rstd ? rstd + t0 : nullptr;
-        const hipError_t e =
-            s.dtype == MOE_BF16
-                ? launch_norm<true>(part, at(x, row), at(residual, row), weight, eps, at(s_out, row), at(y, row),
-                                    at(q, s.H), at(scales, s.H / moe::kMxBlock), rs, st)
-                : launch_norm<false>(part, at(x, row), at(residual, row), weight, eps, at(s_out, row), at(y, row),
-                                     at(q, s.H), at(scales, s.H / moe::kMxBlock), rs, st);
+        const hipError_t e = launch(part, at(x, row), at(residual, row), weight, eps, at(s_out, row), at(y, row),
+                                    at(q, s.H), at(scales, s.H / moe::kMxBlock), rstd ? rstd + t0 : nullptr, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -489,9 +488,11 @@ hipError_t moe_launch_rmsnorm_backward(const moe_shape_t& s, const void* s_in, c
 {
     const int G = moe::norm_bwd_groups(s);
     if (G > 0) {
-        const hipError_t e = s.dtype == MOE_BF16
-                                 ? launch_norm_bwd<true>(s, s_in, weight, rstd, dy, ds, dx, part, G, st)
-                                 : launch_norm_bwd<false>(s, s_in, weight, rstd, dy, ds, dx, part, G, st);
+        const int64_t row = (int64_t)s.H * (s.dtype == MOE_BF16 ? 2 : 4);
+        const bool stream = s.T * row * (3 + !!ds) > moe::kStreamBytes;
+        auto* launch = s.dtype == MOE_BF16 ? (stream ? launch_norm_bwd<true, true> : launch_norm_bwd<true, false>)
+                                           : (stream ? launch_norm_bwd<false, true> : launch_norm_bwd<false, false>);
+        const hipError_t e = launch(s, s_in, weight, rstd, dy, ds, dx, part, G, st);
         if (e != hipSuccess) return e;
     }
     for (int64_t h0 = 0; h0 < s.H; h0 += (int64_t)kMaxRows * kRedCols) {

@@ -130,6 +130,52 @@ def test_rmsnorm_more_rows_than_one_launch_takes():
     assert int((y != 0).any(-1).sum()) == len(some) and bool((rstd > 0).all())
 
 
+@pytest.mark.parametrize("t,H", [(BF, 4160), (BF, 576), (F32, 2080)], ids=["bf16", "bf16_narrow", "f32"])
+def test_norms_past_the_caches(t, H):
+    """Calls of more than 256 MB (their accesses are streamed) give the bits of
+    the same rows in calls of 1000, in place as well."""
+    T = 300_000_000 // (H * 4 * (2 if t == BF else 4)) + 7
+    say("norms past the caches", T, H, t)
+    g = gen(H)
+    x, r, dy = (randn(g, T, H).to(t) for _ in range(3))
+    w = (1 + 0.3 * randn(g, H)).to(t)
+
+    def outs(n):
+        return dict(s=torch.empty(n, H, dtype=t, device=DEV), y=torch.empty(n, H, dtype=t, device=DEV),
+                    q=torch.empty(n, H, dtype=torch.uint8, device=DEV),
+                    scales=torch.empty(n, H // 32, dtype=torch.uint8, device=DEV), rstd=torch.empty(n, device=DEV))
+
+    big = outs(T)
+    moe.moe_rmsnorm(norm_shape(T, H, t), x, w, EPS, residual=r, **big)
+    dx, dw, dw1 = torch.empty_like(x), torch.empty(H, device=DEV), torch.empty(H, device=DEV)
+
+    def back(n, s, rstd, dyn, ds, out, dwn):
+        sh = norm_shape(n, H, t)
+        ws = torch.empty(moe.moe_rmsnorm_backward_workspace_bytes(sh), dtype=torch.uint8, device=DEV)
+        moe.moe_rmsnorm_backward(sh, s, w, rstd, dyn, out, dwn, ws, ds=ds)
+
+    back(T, big["s"], big["rstd"], dy, r, dx, dw)
+    total = torch.zeros(H, dtype=torch.float64, device=DEV)
+    for i in range(0, T, 1000):
+        n = min(1000, T - i)
+        rows, o = slice(i, i + n), outs(n)
+        moe.moe_rmsnorm(norm_shape(n, H, t), x[rows], w, EPS, residual=r[rows], **o)
+        for name in o:
+            assert torch.equal(big[name][rows], o[name]), (name, i)
+        part = torch.empty(n, H, dtype=t, device=DEV)
+        back(n, o["s"], o["rstd"], dy[rows], r[rows], part, dw1)
+        assert torch.equal(dx[rows], part), i
+        total += dw1.double()
+    # each sum adds in float32: up to T / 512 rows in turn, then 512 partial sums in 16 + 16 steps
+    mag = (dy.double() * big["s"].double() * big["rstd"].double()[:, None]).abs().sum(0)
+    assert bool(((dw.double() - total).abs() <= 2 * (T / 512 + 64) * ref.U * mag).all())
+    a, b, d = x.clone(), r.clone(), dy.clone()
+    moe.moe_rmsnorm(norm_shape(T, H, t), a, w, EPS, residual=b, s=b, y=a)
+    assert torch.equal(b, big["s"]) and torch.equal(a, big["y"])
+    back(T, big["s"], big["rstd"], d, r, d, dw1)
+    assert torch.equal(d, dx) and torch.equal(dw1, dw)
+
+
 def test_rmsnorm_nonfinite_rows_stay_apart():
     T, H = 6, 256
     g = gen(5)
@@ -586,6 +632,25 @@ def test_grad_clip_views_at_odd_offsets():
         moe.moe_grad_clip(grads, into, 0.5, norm)
         c = 0.5 / float(norm)
         assert bool(((into[0].double() - grads[0].double() * c).abs() <= grads[0].double().abs() * c * 3.01 * ref.U + 1e-40).all())
+
+
+def test_grad_clip_past_the_caches():
+    """A list of more than 256 MB: its norm against float64, and the clip's bits
+    against the same tensors' in lists of one."""
+    g = gen(31)
+    big = [randn(g, 40_000_003), randn(g, 30_000_001).to(BF), randn(g, 25_000_000)[1:], randn(g, 7).to(BF)]
+    norm, err = grad_norm(big)
+    want = math.sqrt(sum(float(t.double().pow(2).sum()) for t in big))
+    assert err == 0 and abs(float(norm) - want) <= want * 2 * ref.U
+    into = [torch.empty_like(t) for t in big]
+    moe.moe_grad_clip(big, into, 1.0, norm)
+    for t, o in zip(big, into):
+        one = [torch.empty_like(t)]
+        moe.moe_grad_clip([t], one, 1.0, norm)
+        assert torch.equal(o, one[0])
+    moe.moe_grad_clip(big, big, 1.0, norm)
+    for t, o in zip(big, into):
+        assert torch.equal(t, o)
 
 
 def test_grad_norm_ranges_and_nonfinite():
