@@ -366,6 +366,7 @@ struct Unit {
 
 struct Gemm {
     int E, ntn, H, F, P, base;  // base: kind of an expert's whole tiles
+    int split;                  // tiles may be cut along K
     const uint8_t *a, *as;
     const int32_t *sched, *vrow;
     const uint8_t *w0, *s0, *w1, *s1;
@@ -402,7 +403,7 @@ __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 #pragma unroll
     for (int k = 0; k < kMxKinds; ++k)
         if (k <= kind) {
-            w = kind_work(n[k], first, g.P, KT, total < kSplitRounds * g.P);
+            w = kind_work(n[k], first, g.P, KT, g.split && total < kSplitRounds * g.P);
             first += w.count;
         }
     return w;
@@ -1237,6 +1238,16 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
     ring_tiles<MODE, 3>(g, lds, slot_id);
 }
 
+// Whether a launch may cut tiles along K: not where the rows alone make
+// kSplitRounds rounds of tiles, whatever their experts (the fixup then need not
+// be launched, 5 us), nor where K has no two parts.
+inline bool may_split(const moe_shape_t& s, int mode, int P)
+{
+    const int64_t N = (int64_t)s.T * s.k, ntn = mode == kGateUp ? s.F / (kTN / 2) : (s.H + kTN - 1) / kTN;
+    const int KT = (mode == kGateUp ? s.H : s.F) / kTK, top = mx_rows(moe::mx_base(s));
+    return KT >= 2 * moe::kMxMinStages && (N + top - 1) / top * ntn < (int64_t)kSplitRounds * P;
+}
+
 // Adds the K-parts of split tiles in order: workgroup (tile, token block) of
 // a kind, its waves as the tile's.
 //
@@ -1247,8 +1258,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 inline int fix_items(const moe_shape_t& s, int mode, int kind, int P)
 {
     const int base = moe::mx_base(s), tb = kind == 0 ? 4 : mx_rows(kind) / 32;
-    const int KT = (mode == kGateUp ? s.H : s.F) / kTK;
-    if (kind < base || KT < 2 * moe::kMxMinStages) return 0;
+    if (kind < base) return 0;
     if (kind < kMxKinds - 1 && (int64_t)s.T * s.k <= mx_rows(kind + 1)) return 0;
     const int ntn = mode == kGateUp ? s.F / (kTN / 2) : (s.H + kTN - 1) / kTN;
     const int64_t tiles = moe::mx_tiles(s, kind) * ntn;
@@ -1306,6 +1316,7 @@ __global__ __launch_bounds__(kThreads) void mx_fixup_kernel(const Gemm g, const 
 template <int MODE>
 hipError_t launch_fixup(const Gemm& g, const moe_shape_t& s, hipStream_t st)
 {
+    if (!g.split) return hipSuccess;
     FixGrid f;
     int n = 0;
     for (int k = 0; k < kMxKinds; ++k) f.end[k] = n += fix_items(s, MODE, k, g.P);
@@ -1356,6 +1367,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.y = static_cast<uint16_t*>(y);
     for (int k = 0; k < kMxKinds; ++k) g.part[k] = reinterpret_cast<float*>(ws + W.part[k]);
     g.ntn = s.F / (kTN / 2);
+    g.split = may_split(s, kGateUp, g.P);
     g.a = static_cast<const uint8_t*>(a);
     g.as = static_cast<const uint8_t*>(a_s);
     g.w0 = w.gate;
@@ -1366,6 +1378,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_fixup<kGateUp>(g, s, st)) != hipSuccess) return e;
     g.ntn = (s.H + kTN - 1) / kTN;
+    g.split = may_split(s, kDown, g.P);
     g.a = g.h;
     g.as = g.hs;
     g.w0 = w.down;
