@@ -220,7 +220,8 @@ struct Bf16x16 {
 template <int B>
 __device__ __forceinline__ Bf16x16 widen(const u32x4& c, uint32_t scales)
 {
-    const float s = __uint_as_float(B == 3 ? (scales >> 1) & 0x7f800000u : (scales << (23 - 8 * B)) & 0x7f800000u);
+    const uint32_t at = B == 3 ? scales >> 1 : scales << (B == 3 ? 0 : 23 - 8 * B);
+    const float s = __uint_as_float(at & 0x7f800000u);
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
