@@ -413,7 +413,8 @@ def test_experts_mx(case):
     assert torch.equal(L.out, again) and torch.equal(L.y, y)       # whatever the workspace held
 
 
-@pytest.mark.parametrize("case", [(4200, 2, 4096), (280, 40, 1024)], ids=["256-row tiles", "32-row tiles"])
+@pytest.mark.parametrize("case", [(4200, 2, 4096), (280, 40, 1024), (6300, 3, 4096), (6200, 9, 4096)],
+                         ids=["256-row tiles", "32-row tiles", "last round in halves", "uneven halves"])
 def test_experts_mx_rows_4_kb_apart(case):
     """Whole rounds of tiles on rows a multiple of 4 KB apart, whose K starts
     are staggered: every row is written, and a sample of them (each tile's ends
@@ -422,7 +423,7 @@ def test_experts_mx_rows_4_kb_apart(case):
     H = 4096
     say("experts_mx", case)
     g = gen(T)
-    L = MoeLayerMx(moe.Shape(T, H, E, 1, F, 2, 1, moe.MOE_BF16), DEV)
+    L = MoeLayerMx(moe.Shape(T, H, E, 1, F, 2 - E % 2, 1, moe.MOE_BF16), DEV)
     xq, xs = quantized(randn(g, T, H))
     ids, w = choose(g, T, E, 1, 0.0)
     wts = weights(g, E, F, H)
