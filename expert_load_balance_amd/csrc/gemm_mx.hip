@@ -180,7 +180,7 @@ __device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t range)
     r[3] = 0x00020000;                         // data format 32
     return r;
 }
-// STREAM: not kept in the caches (weights that no other workgroup reads).
+// STREAM: not kept in the caches.
 template <bool STREAM = false>
 __device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
 {
@@ -375,10 +375,11 @@ struct Unit {
     int e, n0, rows, x0;   // expert, first weight row, rows, first virtual row
     int k0, KT, pidx;      // K-stages k0 .. k0 + KT; partial tile or -1
     int rot;               // which of them comes first (the others follow, then 0 .. rot - 1)
+    int alone;             // the expert has no other M-tile
 };
 
 struct Gemm {
-    int E, ntn, H, F, P, base;  // base: kind of an expert's whole tiles
+    int E, ntn, H, F, P;
     int split;                  // tiles may be cut along K
     const uint8_t *a, *as;
     const int32_t *sched, *vrow;
@@ -440,6 +441,7 @@ __device__ __forceinline__ void place(const Gemm& g, int t, int e, int t0, int t
     u.n0 = uni(nt * (MODE == kGateUp ? kTN / 2 : kTN));
     u.rows = uni(min(height, c - v0));
     u.x0 = uni(r0 + v0);
+    u.alone = uni(mts == 1);
 }
 
 // The tile's expert by the prefix of tiles: scalar loads, which do not wait
@@ -576,6 +578,18 @@ constexpr int max4(int a, int b, int c, int d)
 constexpr int kLds = max4(Geo<kGateUp, 0>::kBytes, Geo<kGateUp, 1>::kBytes, Geo<kGateUp, 2>::kBytes,
                           Geo<kGateUp, 3>::kBytes);
 
+// Weights that one tile reads are streamed past the caches, those that the
+// expert's other M-tiles read too are kept. Tiles below the launch's whole ones
+// (mx_base) are their expert's only tile: gate/up of 128 x 16 rows of 4096 x 1536
+// 279 -> 261 us streamed, of 256 x 32 rows of 7168 x 2048 1404 -> 1320 us. 256-row
+// tiles are kept (streamed, the 256-expert layer's gate/up took 2437 us for 2331).
+// Whole tiles of 128 rows (H or F below 512) are either, so there each expert goes
+// by its own tiles (both projections, beside all kept / all streamed): 16 tiles of
+// each of 8 experts of 4096 x 384 156 us (154 / 177), two of each of 256 experts of
+// 7168 x 384 1187 us (1164 / 1221), two of each of 64 of 256 x 8192 348 us (347 / 340),
+// one of each of 128 of 4096 x 384 170 us (195 / 169).
+enum Weights { kKept, kStreamed, kByExpert };
+
 // Copies of a unit's stages. The stages of a workgroup's units of one kind
 // form one stream: stage number n of the stream sits in slot n % kSlots, and
 // the copies run kAhead stages ahead of the products, across units. Past the
@@ -587,14 +601,14 @@ constexpr int kLds = max4(Geo<kGateUp, 0>::kBytes, Geo<kGateUp, 1>::kBytes, Geo<
 // .. 8 q + 7 of an operand, lane l row 8 q + l / 8, chunk l % 8. Scales: 4
 // bytes (a stage's four blocks) of weight row 64 wave + lane and, in the
 // lanes below kRows / 4, of row kRows / 4 * wave + lane.
-template <int MODE, int KIND>
+template <int MODE, int KIND, Weights WEIGHTS>
 struct Copier {
     using GE = Geo<MODE, KIND>;
     const char *ab, *wb0, *wb1, *asb, *sb;  // rows, weight blocks 0..3 and 4..7, scales
     int upper;                              // down: weight rows from block 4 on (0 or less: none)
     uint32_t aoff[GE::kACopies], woff, asoff, wsoff;
     int rows32;        // bytes of 32 weight rows
-    int rot;
+    int rot, alone;
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
 
     // list: the unit's row list in LDS (gate/up; down reads h in virtual order)
@@ -613,6 +627,7 @@ struct Copier {
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + u.k0 * 4);
         st = scalar<0>();
         rot = u.rot;
+        if (WEIGHTS == kByExpert) alone = u.alone;
         real = u.KT;
         KT = GE::stream_stages(u.KT);
         // (looked up for padding rows too: as a load under a condition it would be
@@ -657,13 +672,10 @@ struct Copier {
     {
         copy16(buffer_of(ab, range()), aoff[i], ks() * kTK, slot + wave * 1024 + i * 4096);
     }
+    template <bool STREAM>
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
     {
-        // An expert's one small tile reads its weights once: gate/up of 128 x 16
-        // rows of 4096 x 1536 279 -> 261 us, of 256 x 32 rows of 7168 x 2048 1404 ->
-        // 1320 us. 256-row tiles share theirs with the expert's other tiles
-        // (streamed, the 256-expert layer's gate/up took 2437 us for 2331).
-        copy16<KIND != 0>(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
+        copy16<STREAM>(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
                ks() * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
@@ -673,8 +685,13 @@ struct Copier {
     }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
+        if (WEIGHTS == kStreamed || (WEIGHTS == kByExpert && alone)) {
 #pragma unroll
-        for (int i = 0; i < kWCopies; ++i) weight(i, slot + GE::kA + i * 4096, wave);
+            for (int i = 0; i < kWCopies; ++i) weight<true>(i, slot + GE::kA + i * 4096, wave);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWCopies; ++i) weight<false>(i, slot + GE::kA + i * 4096, wave);
+        }
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) row(i, slot, wave);
         scales(sslot, wave, lane);
@@ -754,7 +771,7 @@ __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
 // Bound by streaming the weights: a ring of up to four stages, one barrier per
 // stage, the fragments read as the products need them. 128 experts of 16 rows
 // of 4096 x 1536: 5.3 TB/s of weights, where a plain read of 4 GB reaches 6.2.
-template <int MODE, int KIND>
+template <int MODE, int KIND, Weights WEIGHTS>
 __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id)
 {
     using GE = Geo<MODE, KIND>;
@@ -791,7 +808,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     }
     wait_vm_lgkm<0>();
     slot_barrier();
-    Copier<MODE, KIND> cp;
+    Copier<MODE, KIND, WEIGHTS> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0;       // this unit's number
     int at = 0;      // slot of the stage being computed
@@ -1028,7 +1045,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     auto kept = [&](int m) {
         const int4* p = reinterpret_cast<const int4*>(lds + GE::kKept0) + (wave * 3 + m % 3) * 2;
         const int4 a = p[0], b = p[1];
-        return Unit{uni(a.x), uni(a.y), uni(a.z), uni(a.w), uni(b.x), uni(b.y), uni(b.z), uni(b.w)};
+        return Unit{uni(a.x), uni(a.y), uni(a.z), uni(a.w), uni(b.x), uni(b.y), uni(b.z), uni(b.w), 0};
     };
     Unit u = unit_of<MODE, 0, true>(g, work, unit_at(g, 0));
     copy_list<0>(g, u, list_u(0), wave, lane);
@@ -1039,7 +1056,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     }
     wait_vm_lgkm<0>();
     slot_barrier();
-    Copier<MODE, 0> cp;
+    Copier<MODE, 0, kKept> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0, odd = 0;  // this unit's number; parity of the stage being computed
     constexpr int kEarly = 4;  // weight copies in a stage's first half (one unit)
@@ -1132,7 +1149,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     for (int n = 0; n < 2; ++n) {
         follow();
 #pragma unroll
-        for (int i = 0; i < kWCopies; ++i) cp.weight(i, unit_u(2 * n + i / 4, i), wave);
+        for (int i = 0; i < kWCopies; ++i) cp.template weight<false>(i, unit_u(2 * n + i / 4, i), wave);
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) cp.row(i, slot_u(n), wave);
         ++cp.st;
@@ -1197,7 +1214,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
                 for (int z = 0; z < 4 + NB; ++z)
                     if (read_at(z, kM) == q) read(odd, wat, 1, z);
 #pragma unroll
-                for (int z = q * kEarly / kM; z < (q + 1) * kEarly / kM; ++z) cp.weight(z, unit_u(wcopy, z), wave);
+                for (int z = q * kEarly / kM; z < (q + 1) * kEarly / kM; ++z) cp.template weight<false>(z, unit_u(wcopy, z), wave);
                 __builtin_amdgcn_sched_barrier(0);
             }
             wait_vm_lgkm<kEarly>();
@@ -1210,7 +1227,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
                 for (int z = q * 12 / kM; z < (q + 1) * 12 / kM; ++z) {
                     if (z < GE::kACopies) cp.row(z, sl, wave);
                     else if (z - GE::kACopies < kWCopies - kEarly)
-                        cp.weight(kEarly + z - GE::kACopies, unit_u(wcopy1, z), wave);
+                        cp.template weight<false>(kEarly + z - GE::kACopies, unit_u(wcopy1, z), wave);
                 }
 #pragma unroll
                 for (int z = 0; z < 8; ++z)
@@ -1251,16 +1268,17 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     }
 }
 
-template <int MODE>
+// BASE: kind of an expert's whole tiles (mx_base)
+template <int MODE, int BASE>
 __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 {
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const int b = blockIdx.x;
     const int slot_id = b % 8 * (g.P / 8) + b / 8;
-    big_tiles<MODE>(g, lds);
-    ring_tiles<MODE, 1>(g, lds, slot_id);
-    ring_tiles<MODE, 2>(g, lds, slot_id);
-    ring_tiles<MODE, 3>(g, lds, slot_id);
+    if constexpr (BASE == 0) big_tiles<MODE>(g, lds);
+    ring_tiles<MODE, 1, BASE == 0 ? kStreamed : kByExpert>(g, lds, slot_id);
+    ring_tiles<MODE, 2, kStreamed>(g, lds, slot_id);
+    ring_tiles<MODE, 3, kStreamed>(g, lds, slot_id);
 }
 
 // Whether a launch may cut tiles along K: not where the rows alone make
@@ -1371,12 +1389,12 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
                                       const int32_t* plan, const MoeMxWeights& w, void* y,
                                       char* ws, hipStream_t st)
 {
-    const int N = s.T * s.k;
+    const int N = s.T * s.k, base = moe::mx_base(s);
     if (N == 0) return hipSuccess;
     const moe::MxWsLayout W = moe::mx_ws_layout(s);
     int32_t* sched = reinterpret_cast<int32_t*>(ws + W.sched);
     int32_t* vrow = reinterpret_cast<int32_t*>(ws + W.vrow);
-    mx_schedule_kernel<<<(N + kThreads - 1) / kThreads, kThreads, 0, st>>>(s.E, s.R, N, moe::mx_base(s), plan, sched, vrow);
+    mx_schedule_kernel<<<(N + kThreads - 1) / kThreads, kThreads, 0, st>>>(s.E, s.R, N, base, plan, sched, vrow);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     Gemm g;
@@ -1384,7 +1402,6 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.H = s.H;
     g.F = s.F;
     g.P = persistent_grid();
-    g.base = moe::mx_base(s);
     g.sched = sched;
     g.vrow = vrow;
     g.h = reinterpret_cast<uint8_t*>(ws + W.h);
@@ -1399,7 +1416,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.s0 = w.gate_s;
     g.w1 = w.up;
     g.s1 = w.up_s;
-    gemm_mx_kernel<kGateUp><<<g.P, kThreads, 0, st>>>(g);
+    (base == 0 ? gemm_mx_kernel<kGateUp, 0> : gemm_mx_kernel<kGateUp, 1>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_fixup<kGateUp>(g, s, st)) != hipSuccess) return e;
     g.ntn = (s.H + kTN - 1) / kTN;
@@ -1409,7 +1426,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.w0 = w.down;
     g.s0 = w.down_s;
     g.w1 = g.s1 = nullptr;
-    gemm_mx_kernel<kDown><<<g.P, kThreads, 0, st>>>(g);
+    (base == 0 ? gemm_mx_kernel<kDown, 0> : gemm_mx_kernel<kDown, 1>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     return launch_fixup<kDown>(g, s, st);
 }

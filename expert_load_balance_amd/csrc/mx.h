@@ -73,7 +73,8 @@ constexpr int kMxMinStages = 4;  // of a K-part
 __host__ __device__ constexpr int mx_rows(int kind) { return 256 >> kind; }
 
 // Kind of an expert's whole tiles: the 256-row kernel reads its scales 16
-// bytes (512 values of K) at a time.
+// bytes (512 values of K) at a time. One schedule serves both projections, so the
+// shorter K decides for both.
 __host__ inline int mx_base(const moe_shape_t& s) { return s.H >= 512 && s.F >= 512 ? 0 : 1; }
 
 // Upper bound on the tiles of one kind: experts of this kind, one tile each,
