@@ -31,13 +31,14 @@ moe_status_t check_mx(const moe_shape_t* s)
 
 inline int elem(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
+// pointers: the types and sources too (the size query's lists need not have any)
 moe_status_t check_grads(int32_t n, const moe_grad_t* g, bool pointers, bool with_dst)
 {
     if (n < 0 || (n > 0 && !g)) return MOE_EINVAL;
     for (int32_t i = 0; i < n; ++i) {
         if (g[i].count < 0 || g[i].count >= (int64_t(1) << 40)) return MOE_EINVAL;
-        if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return MOE_EINVAL;
         if (!pointers) continue;
+        if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return MOE_EINVAL;
         if (bad(g[i].src, g[i].count, elem(g[i].dtype))) return MOE_EINVAL;
         if (with_dst && bad(g[i].dst, g[i].count, elem(g[i].dtype))) return MOE_EINVAL;
     }
