@@ -47,7 +47,6 @@ moe_status_t check_grads(int32_t n, const moe_grad_t* g, bool pointers, bool wit
 
 struct Span {
     uintptr_t lo, hi;
-    int owner;
     bool write;
 };
 int by_lo(const void* a, const void* b)
@@ -70,10 +69,10 @@ moe_status_t check_overlap(int32_t n, const moe_grad_t* g)
         if (g[i].count == 0) continue;
         const uintptr_t len = (uintptr_t)g[i].count * elem(g[i].dtype);
         const uintptr_t s = reinterpret_cast<uintptr_t>(g[i].src), d = reinterpret_cast<uintptr_t>(g[i].dst);
-        sp[m++] = Span{d, d + len, i, true};
+        sp[m++] = Span{d, d + len, true};
         if (s != d) {
             hit = s < d + len && d < s + len;
-            sp[m++] = Span{s, s + len, i, false};
+            sp[m++] = Span{s, s + len, false};
         }
     }
     if (!hit) {
