@@ -28,6 +28,15 @@ def alloc(shape, dtype, device):
     return torch.empty(max(n, 1), dtype=dtype, device=device)[:n].view(shape)
 
 
+def _check_here(*tensors):
+    """The layer's kernels run on the current device; the calls that come first
+    do not look where their tensors are."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor of the layer is on {t.device}, the current device is cuda:{here}")
+
+
 class MoeLayerBuffers:
     """Every buffer of one layer call, sized by the shape alone.
 
@@ -184,6 +193,7 @@ class MoeLayerMx:
         the 8-bit rows and the router's choice (ids, gate weights w) to
         self.out."""
         s, st = self.shape, stream if stream is not None else torch.cuda.current_stream()
+        _check_here(self.err, ids, w, shared_y)
         moe_count_plan(s, ids, self.counts, self.offsets, self.eidx, self.rank_load, self.err,
                        self.ws, self.plan, st)
         moe_permute_mx(s, xq, xs, ids, self.eidx, self.plan, self.buf_q, self.buf_s, self.dest_row,
@@ -198,6 +208,7 @@ class MoeLayerMx:
         """One step: returns (out, s), the experts' sum and the residual stream
         x + residual that it is to be added to (the next norm's residual)."""
         st = stream if stream is not None else torch.cuda.current_stream()
+        _check_here(self.err, w_router, bias)
         with torch.cuda.stream(st):
             self.err.zero_()
         moe_rmsnorm(self.shape, x, norm_weight, eps, residual=residual, s=self.s, y=self.xn,
