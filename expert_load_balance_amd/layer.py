@@ -37,6 +37,14 @@ def _check_here(*tensors):
             raise ValueError(f"a tensor of the layer is on {t.device}, the current device is cuda:{here}")
 
 
+def _torch_stream(stream):
+    """torch's object for a stream or its handle (an ExternalStream of handle 0
+    would be a new stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+
+
 class MoeLayerBuffers:
     """Every buffer of one layer call, sized by the shape alone.
 
@@ -209,7 +217,7 @@ class MoeLayerMx:
         x + residual that it is to be added to (the next norm's residual)."""
         st = stream if stream is not None else torch.cuda.current_stream()
         _check_here(self.err, w_router, bias)
-        with torch.cuda.stream(st):
+        with torch.cuda.stream(_torch_stream(st)):
             self.err.zero_()
         moe_rmsnorm(self.shape, x, norm_weight, eps, residual=residual, s=self.s, y=self.xn,
                     q=self.xq, scales=self.xs, stream=st)

@@ -63,6 +63,7 @@ def test_layer_refuses_another_device_before_any_launch(monkeypatch, which):
     for name in ("moe_rmsnorm", "moe_router", "moe_count_plan", "moe_permute_mx", "moe_grouped_gemm_mx", "moe_combine"):
         monkeypatch.setattr(layer, name, lambda *a, _n=name, **k: calls.append(_n))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: None)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: __import__("contextlib").nullcontext())
     L = layer.MoeLayerMx(moe.Shape(4, 128, 8, 2, 128, 4, 2, moe.MOE_BF16), "cpu")
     L.err = _Elsewhere(1 if which == "err" else 0)
