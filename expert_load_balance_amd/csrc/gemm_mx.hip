@@ -39,9 +39,17 @@
 //   32768 rows of 128 experts, 2048 x 768 163 and 106   (1.27 and 0.98 PFLOP/s)
 //   4094 rows of 8 experts, 4096 x 14336  564 and 276   (1.71 and 1.74 PFLOP/s)
 //   65536 rows of 256 experts, 7168 x 2048 2289 and 1270 (1.68 and 1.52 PFLOP/s)
-// The first two are bound by streaming the weights, the last two by the power
-// of the matrix pipes (see the 256-row tiles below), the middle one by both:
-// six to sixteen stages a tile do not hide its cold start and its epilogue.
+// The first two are bound by streaming the weights. The last two are bound by
+// copies and products that overlap in part only, at a clock that the chip's power
+// holds down (see the 256-row tiles below). In the middle one six to sixteen
+// stages a tile hide neither its cold start nor its epilogue, which takes 5 to 7 us a
+// tile: the vector unit's silu and quantisation of 128 values a lane in gate/up
+// (whose 32 KB of a tile are no load on the memory), y's writes in down.
+//
+// Registers: the 256-row kernels fill the vector registers (243 and 251 and 256
+// accumulators) and spill 128 (gate/up) and 116 (down) scalars to lanes of vector
+// registers, held across a tile's stages for the code between tiles; the stages'
+// own addresses are not among them. The down kernels keep 20 bytes a lane in scratch.
 #include <type_traits>
 
 #include "lds_pipe.h"
@@ -299,7 +307,11 @@ __device__ __forceinline__ void store_h(const f32x16& g, const f32x16& u, __amdg
     __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, hs, (int)(half ? kZeroRow : soff), 0, 0);
 }
 
-// y of one token's 32-column block: 8 consecutive bf16 columns per store.
+// y of one token's 32-column block: 8 consecutive bf16 columns per store. bf16,
+// since y is the combine's input, which has the layer's type: fp32 rows would
+// double the down projection's writes and the combine's reads (0.94 GB each for
+// 65536 rows of 7168). The combine adds in fp32 and rounds its sum again, so
+// its output is 0.0024 of its norm off where one rounding is 0.0017.
 __device__ __forceinline__ void store_y(const f32x16& a, __amdgpu_buffer_rsrc_t y, uint32_t off)
 {
 #pragma unroll
@@ -777,9 +789,9 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     using GE = Geo<MODE, KIND>;
     // Gate and up of up to 64 rows are multiplied in bf16, which is exact: the
     // 8-bit instruction's cut leaves g and u about 1e-4 off, which sends 0.2 %
-    // of h's codes to the other side of their rounding (y's relative error 0.0030,
-    // 0.0023 with exact g and u, 0.0017 of it bf16's own). Beside the weights'
-    // streaming the slower products cost nothing at these sizes. On 128 rows they
+    // of h's codes to the other side of their rounding (y is then 0.0024 of its norm
+    // off, with exact g and u 0.0017, which is bf16's rounding alone). Beside the
+    // weights' streaming the slower products cost nothing at these sizes. On 128 rows they
     // would: 256 x 128 rows of 7168 x 2048 1585 -> 2423 us. The down projection's
     // cut reaches y without a rounding in between, and exact products there
     // would take 1 % on 32-row tiles and 10 % on 64 (256 x 64 rows: 748 -> 827 us).
@@ -943,13 +955,18 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 // (All copies in one half took 2.5 us a stage: the waves that issue them wait
 // for the copy path, and their MFMAs with them.)
 //
-// Measured on random codes: 1.9 to 2.1 us a stage whether the weights come from
-// HBM or from the L2, the matrix pipes busy 62 to 75 % of the cycles at a clock
-// of 1.3 to 1.65 GHz. The chip's power is the bound: taking the ring's address
-// arithmetic out of the loop (units of 32 rows before, 270 instructions beside
-// the products, now 192) cut 3020 cycles a stage to 2730 and the clock from
-// 1.50 to 1.31 GHz with them; 8 experts of 512 rows of 4096 x 14336 went from
-// 519 to 484 us (gate/up, 1.99 PFLOP/s) and from 245 to 232 us (down).
+// Measured in a stream of calls, once the clock has settled (counters of cycles
+// and of time read inside the kernel; tile ends included in the stages): 8 experts
+// of 512 rows of 4096 x 14336, gate/up, 3230 cycles at 1.81 GHz = 1.78 us a stage, 63 %
+// of them products; the same with codes random in every bit 3150 at 1.67 GHz; the
+// 256-expert layer 3210 at 1.88 GHz. In the first calls after idle the clock is lower
+// (1.5 to 1.75 GHz) and a stage has fewer cycles (2850 to 3180). So it is two things:
+// power holds the clock below the 2.2 GHz of the short-K layers, and what does not
+// follow the clock, a stage's 64 KB of copies (37 GB/s a CU here, 52 to 56 where a
+// CU only copies), overlaps the products in part only. Fewer scalar instructions
+// beside the products (the ring's units of 128 rows for 32) took 8 experts of 512 rows
+// of 4096 x 14336 from 519 to 484 us (gate/up) and from 245 to 232 us (down), in calls
+// of random codes at the lower clock.
 //
 // One wave's vector memory instruction costs as much for 64 lines of 16 bytes as
 // for a kilobyte in 8: copies of 4 bytes of scales a stage for each of the 512

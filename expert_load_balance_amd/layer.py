@@ -160,7 +160,9 @@ class MoeLayerMx:
 
     A shape whose dtype is MOE_BF16 with H and F multiples of 128. Weights are
     (codes, scales) pairs as moe_mx_quantize makes them. The buffers belong to
-    one call at a time: calls that may overlap take an object each.
+    one call at a time: calls that may overlap take an object each. A layer with a
+    shared expert makes forward's calls itself and hands that expert's rows, made
+    from self.xn, to experts.
     """
 
     def __init__(self, shape: Shape, device="cuda"):

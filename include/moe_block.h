@@ -99,7 +99,9 @@ size_t moe_mx_workspace_bytes(const moe_shape_t *shape);
  * the largest and cut them at 2^-13 of its power of two (sums then carry about
  * 18 bits): where g and u come from such sums (experts of more than 64 rows), a
  * value of h next to the border of two codes may take either. Products and
- * values below 2^-126 may be taken as zero.
+ * values below 2^-126 may be taken as zero. So the bits of a row's y go by its
+ * batch: by whether its expert has up to 64 rows there, and by the parts that the
+ * launch cuts K into. Calls on the same inputs repeat theirs.
  *   d_a, d_a_scales uint8[N][H], uint8[N][H/32] (moe_permute_mx's buffer);
  *   d_w_gate, d_w_up uint8[E][F][H] with scales uint8[E][F][H/32];
  *   d_w_down uint8[E][H][F] with scales uint8[E][H][F/32]; d_plan from
@@ -116,7 +118,8 @@ moe_status_t moe_grouped_gemm_mx(const moe_shape_t *shape, const void *d_a, cons
 /* One gradient of a list. The list is host memory, read before the call
  * returns; tensors may be empty (src and dst then may be NULL). */
 typedef struct moe_grad {
-    const void *src; /* device dtype[count], aligned to its element size      */
+    const void *src; /* device dtype[count], aligned to its element size (one
+                        off 16 bytes takes 1.2 to 6 times as long)            */
     void *dst;       /* moe_grad_clip: device dtype[count], may be src        */
     int64_t count;   /* elements, 0 <= count < 2^40                           */
     int32_t dtype;   /* moe_dtype_t                                           */
