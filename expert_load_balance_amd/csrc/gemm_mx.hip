@@ -33,12 +33,13 @@
 // rounds up it gained what the fixup cost): each part stores its fp32 tile in
 // fragment order, and mx_fixup_kernel adds the parts in order and finishes.
 //
-// Measured (us, gate/up then down, whole launches without the fixups):
-//   8 rows of 8 experts, 4096 x 1536      26 and 13     (3.9 TB/s of weights)
-//   2048 rows of 128 experts, 4096 x 1536 304 and 156   (5.3 and 5.2 TB/s)
-//   32768 rows of 128 experts, 2048 x 768 163 and 106   (1.27 and 0.98 PFLOP/s)
-//   4094 rows of 8 experts, 4096 x 14336  564 and 276   (1.71 and 1.74 PFLOP/s)
-//   65536 rows of 256 experts, 7168 x 2048 2289 and 1270 (1.68 and 1.52 PFLOP/s)
+// Measured (us, gate/up then down, whole launches without the fixups, in a stream
+// of calls once the clock has settled):
+//   8 rows of 8 experts, 4096 x 1536      26 and 14     (3.9 TB/s of weights)
+//   2048 rows of 128 experts, 4096 x 1536 273 and 149   (6.1 and 5.6 TB/s)
+//   32768 rows of 128 experts, 2048 x 768 160 and 103   (1.29 and 1.00 PFLOP/s)
+//   4094 rows of 8 experts, 4096 x 14336  474 and 250   (2.03 and 1.92 PFLOP/s)
+//   65536 rows of 256 experts, 7168 x 2048 2211 and 1214 (1.74 and 1.58 PFLOP/s)
 // The first two are bound by streaming the weights. The last two are bound by
 // copies and products that overlap in part only, at a clock that the chip's power
 // holds down (see the 256-row tiles below). In the middle one six to sixteen
@@ -782,7 +783,7 @@ __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
 // ------------------------------------------------- tiles below 256 rows --
 // Bound by streaming the weights: a ring of up to four stages, one barrier per
 // stage, the fragments read as the products need them. 128 experts of 16 rows
-// of 4096 x 1536: 5.3 TB/s of weights, where a plain read of 4 GB reaches 6.2.
+// of 4096 x 1536: 6.1 TB/s of weights, where a plain read of 4 GB reaches 6.2.
 template <int MODE, int KIND, Weights WEIGHTS>
 __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id)
 {
@@ -958,10 +959,10 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 // Measured in a stream of calls, once the clock has settled (counters of cycles
 // and of time read inside the kernel; tile ends included in the stages): 8 experts
 // of 512 rows of 4096 x 14336, gate/up, 3230 cycles at 1.81 GHz = 1.78 us a stage, 63 %
-// of them products; the same with codes random in every bit 3150 at 1.67 GHz; the
-// 256-expert layer 3210 at 1.88 GHz. In the first calls after idle the clock is lower
-// (1.5 to 1.75 GHz) and a stage has fewer cycles (2850 to 3180). So it is two things:
-// power holds the clock below the 2.2 GHz of the short-K layers, and what does not
+// of them products; the same with codes random in every bit 3150 at 1.67 GHz; 4094
+// rows of them unevenly, 3090 at 1.95 GHz (58 %). In the first calls after idle the
+// clock is lower (1.5 to 1.75 GHz) and a stage has fewer cycles (2800 to 3180). So it
+// is two things: power holds the clock below the 2.2 GHz of the short-K layers, and what does not
 // follow the clock, a stage's 64 KB of copies (37 GB/s a CU here, 52 to 56 where a
 // CU only copies), overlaps the products in part only. Fewer scalar instructions
 // beside the products (the ring's units of 128 rows for 32) took 8 experts of 512 rows
