@@ -78,7 +78,8 @@ def norm(x, residual, w, eps):
 
 
 def norm_rel(H):
-    """Relative error of rstd and of v in float32: a thread adds up to
+    """Relative error of rstd and of v where the squares are added in float32 (the
+    kernel adds them in fp64, far within this): a thread adds up to
     max(4 * 8, H / 1024) squares in turn, then 6 steps of a wave and 16 waves;
     all terms are positive, so each add is off by U of a partial sum that is
     no more than the whole. The mean's error halves in the root; division,
