@@ -1,8 +1,9 @@
 """Python binding of libmoe.so, the MI355X (gfx950) MoE-layer hot path.
 
 Argument marshalling only: every function here has the name of a C entry
-point declared in ``include/moe.h`` (the layer) or ``include/moe_block.h`` (the
-operators around it, bound in ``block.py``), checks that the tensors it is given have
+point declared in ``include/moe.h`` (the layer), ``include/moe_block.h`` (the
+operators around it, bound in ``block.py``) or ``include/moe_step.h`` (bound in
+``step.py``), checks that the tensors it is given have
 the documented dtype, device and contiguity, and passes their device pointers
 and the current HIP stream through ctypes. All arithmetic runs in the HIP
 kernels; there is no CPU path. If the library has not been built, every call
@@ -182,6 +183,7 @@ def load():
                                         _VP, ctypes.c_size_t, _VP]),
     }
     sig.update(block.signatures())
+    sig.update(step.signatures())
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -238,7 +240,9 @@ _HOST_ONLY = frozenset(("moe_status_str", "moe_check_shape", "moe_plan_layout",
                         "moe_workspace_bytes", "moe_router_workspace_bytes", "moe_capacity_rows",
                         "moe_pool_bytes", "moe_backward_workspace_bytes",
                         "moe_replica_grad_bytes", "moe_rmsnorm_backward_workspace_bytes",
-                        "moe_mx_workspace_bytes", "moe_grad_workspace_bytes"))
+                        "moe_mx_workspace_bytes", "moe_grad_workspace_bytes",
+                        "moe_block_norm_backward_workspace_bytes", "moe_mx4_workspace_bytes",
+                        "moe_few_workspace_bytes"))
 
 
 class _Recorder:
@@ -735,7 +739,8 @@ def moe_ffn_backward_replicas(shape, buf, plan, w_gate, w_up, w_down, dy, dbuf, 
         _stream(stream)), "moe_ffn_backward_replicas")
 
 
-from . import block  # noqa: E402
+from . import block, step  # noqa: E402
 from .block import *  # noqa: E402,F401,F403
+from .step import *  # noqa: E402,F401,F403
 
-__all__ += block.__all__
+__all__ += block.__all__ + step.__all__

@@ -1,0 +1,115 @@
+// step.h -- 4-bit blocks on gfx950, sizes of the operators of moe_step.h, and
+// their launchers.
+#pragma once
+
+#include "moe_step.h"
+#include "mx.h"
+
+namespace moe {
+
+// Scale byte of a 4-bit block whose largest magnitude has the bits `top`: the
+// smallest e >= -127 with top <= 6 * 2^e = 1.5 * 2^(e + 2), as e + 127. With
+// top = m * 2^x, m in [1, 2), e is x - 2 where m <= 1.5, else x - 1: adding
+// 0x3fffff carries into the exponent exactly when the mantissa field exceeds
+// 0x400000. Infinities and NaN give 255.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t top)
+{
+    const int e = (int)((top + 0x3fffffu) >> 23) - 2;
+    return top >= 0x7f800000u ? 255u : (uint32_t)(e > 0 ? e : 0);
+}
+
+// Eight e2m1 codes of values divided by the block's scale, first in the low
+// half of the low byte (the quotients are at most 6, the conversion is to
+// nearest even). A scale byte of 255 has codes of 0.
+__device__ __forceinline__ uint32_t mx4_pack8(const float* v, uint32_t byte)
+{
+    const float s = __uint_as_float(byte << 23);  // (taken by its exponent: 0 is 2^-127)
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], s, 3);
+    return byte == 255u ? 0u : r;
+}
+
+// A scale byte's value: 2^-127 is a subnormal, 255 is NaN.
+__device__ __forceinline__ float mx_scale_value(uint32_t byte)
+{
+    return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
+}
+
+// Eight values of e2m1 codes times s.
+__device__ __forceinline__ void mx4_unpack8(uint32_t codes, float s, float* v)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+    v[0] = a[0] * s, v[1] = a[1] * s, v[2] = b[0] * s, v[3] = b[1] * s;
+    v[4] = c[0] * s, v[5] = c[1] * s, v[6] = d[0] * s, v[7] = d[1] * s;
+}
+
+// Rows of the backward of moe_block_norm in parts: a part is a run of
+// neighbouring rows that share one row of gates. kNormBwdGroups workgroups (or
+// as many as there are parts) take parts b, b + G, ...
+struct BlockNormParts {
+    int64_t group_rows, groups;  // rows that share a row of gates, and how many such groups
+    int per_group, part_rows;    // parts of a group, rows of a part (a group's last may be shorter)
+    int64_t parts;
+    int grid;
+};
+inline BlockNormParts block_norm_parts(int64_t T, int32_t gate_rows)
+{
+    BlockNormParts p;
+    p.group_rows = gate_rows > 0 && gate_rows < T ? gate_rows : T > 0 ? T : 1;
+    p.groups = (T + p.group_rows - 1) / p.group_rows;
+    int64_t n = p.groups > 0 ? (kNormBwdGroups + p.groups - 1) / p.groups : 1;
+    if (n > p.group_rows) n = p.group_rows;
+    p.part_rows = (int)((p.group_rows + n - 1) / n);
+    p.per_group = (int)((p.group_rows + p.part_rows - 1) / p.part_rows);
+    p.parts = p.groups * p.per_group;
+    p.grid = (int)(p.parts < kNormBwdGroups ? p.parts : kNormBwdGroups);
+    return p;
+}
+// Workspace: dw_post and dw_pre of each workgroup, then, where groups have
+// several parts, the gate's gradient of each part (fp32 [H] each).
+inline size_t block_norm_bwd_ws(const moe_shape_t& s, int32_t gate_rows)
+{
+    const BlockNormParts p = block_norm_parts(s.T, gate_rows);
+    const size_t rows = 2 * (size_t)(p.grid > 0 ? p.grid : 1) +
+                        (gate_rows > 0 && p.per_group > 1 ? (size_t)p.parts : 0);
+    return align256(rows * s.H * 4);
+}
+
+}  // namespace moe
+
+struct MoeBlockNorm {
+    const void *x, *residual;
+    float alpha;
+    const void *w_post, *gate;
+    int gate_rows;
+    const void* w_pre;
+    float eps;
+    void *s, *y, *q, *scales;
+    float *rstd_post, *rstd_pre;
+};
+struct MoeBlockNormBwd {
+    const void* x;
+    const float* rstd_post;
+    const void* s;
+    const float* rstd_pre;
+    float alpha;
+    const void *w_post, *gate;
+    int gate_rows;
+    const void *w_pre, *dy, *ds;
+    void *dx, *dresidual;
+    float *dw_post, *dgate, *dw_pre;
+};
+hipError_t moe_launch_block_norm(const moe_shape_t& s, const MoeBlockNorm& a, hipStream_t st);
+hipError_t moe_launch_block_norm_backward(const moe_shape_t& s, const MoeBlockNormBwd& a, float* ws,
+                                          hipStream_t st);
+hipError_t moe_launch_mx4_quantize(int64_t rows, int64_t cols, int dtype, const void* x, void* q,
+                                   void* scales, hipStream_t st);
+hipError_t moe_launch_mx4_dequantize(int64_t rows, int64_t cols, int dtype, const void* q,
+                                     const void* scales, void* x, hipStream_t st);

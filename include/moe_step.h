@@ -1,0 +1,108 @@
+/*
+ * moe_step.h -- one step through an MoE layer (moe.h) and between two of
+ * them, in the same library, libmoe.so, under the conventions of moe.h and
+ * moe_block.h:
+ *   moe_block_norm, moe_block_norm_backward
+ *                             what lies between two blocks of a residual
+ *                             stream: the norm behind a block, its gate, the
+ *                             residual's scale and addition, and the norm in
+ *                             front of the next block
+ *   moe_mx4_quantize, moe_mx4_dequantize
+ *                             weights in 4-bit blocks
+ *
+ * 4-bit blocks ("mx4"). As the 8-bit blocks of moe_block.h, 32 consecutive
+ * values of a row to a scale 2^e stored as the byte e + 127, with e2m1 codes
+ * (1 sign, 2 exponent, 1 mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6): e is the
+ * smallest integer >= -127 with max|v| <= 6 * 2^e, so no code saturates, and
+ * each code is v / 2^e rounded to nearest even. Code 2i of a row is the low
+ * half of its byte i. e2m1 has no NaN: a block holding an infinity or NaN gets
+ * the scale byte 255 (NaN) and codes of 0. A matrix of `rows` x `cols`
+ * (cols % 32 == 0) is codes uint8[rows][cols / 2] and scales
+ * uint8[rows][cols / 32].
+ */
+#ifndef MOE_STEP_H
+#define MOE_STEP_H
+
+#include "moe_block.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* T rows of width H (shape->T, H and dtype; the other fields only have to be
+ * valid). x is a block's output, residual the stream that the block read:
+ *   rstd_post = 1 / sqrt(mean(x^2) + eps);  n = x * rstd_post * w_post;
+ *   s = alpha * residual + gate * n         (fp32, rounded once to dtype);
+ *   rstd_pre = 1 / sqrt(mean(s^2) + eps);   v = s * rstd_pre * w_pre  (fp32);
+ *   y = v rounded to dtype;  q, scales = v in 8-bit blocks (moe_block.h).
+ *   d_x dtype[T][H]; d_residual dtype[T][H] or NULL (s = gate * n); alpha
+ *   finite; d_w_post dtype[H] or NULL (n = x, then d_rstd_post is NULL);
+ *   d_gate NULL (1) or, by gate_rows, 0: dtype[T], one value a token, and
+ *   r >= 1: dtype[ceil(T / r)][H], row t / r for token t (1: a gate for every
+ *   value; T or more: one for each channel); d_w_pre dtype[H] or NULL (no
+ *   norm in front: d_y, d_q, d_scales and d_rstd_pre are NULL); eps > 0,
+ *   finite; outputs, each may be NULL (not all of them): d_s, d_y dtype[T][H];
+ *   d_q uint8[T][H] and d_scales uint8[T][H/32] (both or neither; H % 32 == 0,
+ *   MOE_EUNSUPPORTED otherwise); d_rstd_post, d_rstd_pre float[T].
+ * d_s may be d_x or d_residual, and d_y may be d_x or d_residual (not both
+ * outputs the same array). An infinity or NaN stays in its row. */
+moe_status_t moe_block_norm(const moe_shape_t *shape, const void *d_x, const void *d_residual,
+                            float alpha, const void *d_w_post, const void *d_gate,
+                            int32_t gate_rows, const void *d_w_pre, float eps, void *d_s, void *d_y,
+                            void *d_q, void *d_scales, float *d_rstd_post, float *d_rstd_pre,
+                            moe_stream_t stream);
+
+/* Bytes of device workspace moe_block_norm_backward needs (sums of the
+ * weights' and the gate's gradients over parts of the rows). 0 on a bad shape
+ * or gate_rows < 0. Pass 0 where the gate has one value a token or is NULL. */
+size_t moe_block_norm_backward_workspace_bytes(const moe_shape_t *shape, int32_t gate_rows);
+
+/* Backward of moe_block_norm. With shat = s * rstd_pre, xhat = x * rstd_post:
+ *   d = ds + rstd_pre * (dy * w_pre - shat * mean(dy * w_pre * shat));
+ *   dresidual = alpha * d;  dgate = d * n, summed over what a gate multiplied;
+ *   dn = gate * d;
+ *   dx = rstd_post * (dn * w_post - xhat * mean(dn * w_post * xhat));
+ *   dw_pre = sum over rows of dy * shat, dw_post of dn * xhat.
+ * fp32 throughout, dx and dresidual rounded once; sums over rows are added in
+ * an order fixed by the shape and gate_rows.
+ *   d_x, alpha, d_w_post, d_gate, gate_rows, d_w_pre as the forward's; d_s
+ *   dtype[T][H], d_rstd_post, d_rstd_pre float[T] the forward's outputs;
+ *   d_dy dtype[T][H] (the gradient of y) or NULL (none: d_w_pre, d_s,
+ *   d_rstd_pre are not read, d_dw_pre is NULL); d_ds dtype[T][H] (the gradient
+ *   that reaches s past the norm) or NULL; one of the two at least;
+ *   d_w_post NULL: no norm behind (d_rstd_post is not read, d_dw_post NULL);
+ *   outputs: d_dx dtype[T][H]; each may be NULL: d_dresidual dtype[T][H],
+ *   d_dw_post, d_dw_pre float[H], d_dgate float, in d_gate's layout (NULL
+ *   without a gate);
+ *   d_ws / ws_bytes >= moe_block_norm_backward_workspace_bytes(shape,
+ *   gate_rows), gate_rows 0 where d_gate is NULL.
+ * d_dx and d_dresidual may be d_dy or d_ds (not both the same array). */
+moe_status_t moe_block_norm_backward(const moe_shape_t *shape, const void *d_x,
+                                     const float *d_rstd_post, const void *d_s,
+                                     const float *d_rstd_pre, float alpha, const void *d_w_post,
+                                     const void *d_gate, int32_t gate_rows, const void *d_w_pre,
+                                     const void *d_dy, const void *d_ds, void *d_dx,
+                                     void *d_dresidual, float *d_dw_post, float *d_dgate,
+                                     float *d_dw_pre, void *d_ws, size_t ws_bytes,
+                                     moe_stream_t stream);
+
+/* A matrix in 4-bit blocks (weights once, when a model is loaded).
+ *   d_x dtype[rows][cols], dtype a moe_dtype_t; cols % 32 == 0
+ *   (MOE_EUNSUPPORTED otherwise); rows >= 0, cols >= 1, rows * cols < 2^40;
+ *   d_q uint8[rows][cols/2], d_scales uint8[rows][cols/32] out. */
+moe_status_t moe_mx4_quantize(int64_t rows, int64_t cols, int32_t dtype, const void *d_x,
+                              void *d_q, void *d_scales, moe_stream_t stream);
+
+/* The values of 4-bit blocks, code * 2^e rounded to dtype (bf16 holds every
+ * value of magnitude 2^-126 and more exactly; below, bf16's subnormals round). A
+ * scale byte of 255 gives NaN.
+ *   d_q uint8[rows][cols/2], d_scales uint8[rows][cols/32]; d_x
+ *   dtype[rows][cols] out; limits as moe_mx4_quantize. */
+moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const void *d_q,
+                                const void *d_scales, void *d_x, moe_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_STEP_H */
