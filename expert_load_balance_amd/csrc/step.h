@@ -113,3 +113,50 @@ hipError_t moe_launch_mx4_quantize(int64_t rows, int64_t cols, int dtype, const 
                                    void* scales, hipStream_t st);
 hipError_t moe_launch_mx4_dequantize(int64_t rows, int64_t cols, int dtype, const void* q,
                                      const void* scales, void* x, hipStream_t st);
+
+// --------------------------------------------- the layer for a few tokens --
+namespace moe {
+
+constexpr int kFewMaxH = 8192;   // a wave's part of a row of x stays in registers
+constexpr int kFewPart = 4096;   // values of K of a part of the down projection (h in registers, two bf16 each)
+
+inline int few_unit(int form) { return form == MOE_W_BF16 ? 64 : 128; }
+inline int few_parts(int F) { return (F + kFewPart - 1) / kFewPart; }
+
+// logits [T][E], the router's w [N] and each assignment's row [N], h in two bf16
+// planes [N][F] + [T][shared_F], y fp32 [parts][N][H] + [shared parts][T][H]
+struct FewWsLayout {
+    size_t logits, w, row_of, h, y, total;
+    size_t h_shared, h_plane;   // elements: where the shared expert's rows begin, and the second plane
+    size_t y_shared;            // elements
+};
+inline FewWsLayout few_ws_layout(const moe_shape_t& s, int shared_F)
+{
+    const size_t N = (size_t)s.T * s.k, n1 = N > 0 ? N : 1;
+    FewWsLayout w;
+    size_t o = 0;
+    w.logits = o; o = align256(o + ((size_t)s.T * s.E + 1) * 4);
+    w.w = o;      o = align256(o + n1 * 4);
+    w.row_of = o; o = align256(o + n1 * 4);
+    w.h_shared = N * s.F;
+    w.h_plane = w.h_shared + (size_t)s.T * shared_F;
+    w.h = o;      o = align256(o + 2 * w.h_plane * 2);
+    w.y_shared = (size_t)few_parts(s.F) * N * s.H;
+    w.y = o;      o = align256(o + (w.y_shared + (size_t)few_parts(shared_F) * s.T * s.H) * 4);
+    w.total = o;
+    return w;
+}
+
+}  // namespace moe
+
+struct MoeFew {
+    const void *x, *w_router;
+    const float* bias;
+    moe_few_weights_t routed, shared;
+    int form, shared_F;
+    void* out;
+    int32_t* ids;
+    float* w;
+    int32_t* err;
+};
+hipError_t moe_launch_few(const moe_shape_t& s, const MoeFew& a, char* ws, hipStream_t st);

@@ -34,6 +34,25 @@ moe_status_t check_blocks(int64_t rows, int64_t cols, int32_t dtype, const void*
     return bad(x, rows) || bad(q, rows) || bad(scales, rows) ? MOE_EINVAL : MOE_OK;
 }
 
+moe_status_t check_few(const moe_shape_t* s, int32_t form, int32_t shared_F)
+{
+    const moe_status_t st = moe_check_shape(s);
+    if (st != MOE_OK) return st;
+    if ((form != MOE_W_BF16 && form != MOE_W_MX8 && form != MOE_W_MX4) || shared_F < 0) return MOE_EINVAL;
+    const int unit = moe::few_unit(form);
+    if (s->dtype != MOE_BF16 || s->T > MOE_FEW_TOKENS || s->H > moe::kFewMaxH || s->H % unit || s->F % unit ||
+        shared_F % unit)
+        return MOE_EUNSUPPORTED;
+    // (a projection's rows are addressed by 32-bit byte offsets)
+    const int64_t wide = s->F > shared_F ? s->F : shared_F;
+    return wide * s->H * 2 < (int64_t(1) << 32) - 128 ? MOE_OK : MOE_EUNSUPPORTED;
+}
+bool bad_weights(const moe_few_weights_t* w, int32_t form)
+{
+    return !w || bad(w->gate, 1) || bad(w->up, 1) || bad(w->down, 1) ||
+           (form != MOE_W_BF16 && (bad(w->gate_scales, 1) || bad(w->up_scales, 1) || bad(w->down_scales, 1)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -107,6 +126,30 @@ moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const
     const moe_status_t st = check_blocks(rows, cols, dtype, d_x, d_q, d_scales);
     if (st != MOE_OK) return st;
     return dev(moe_launch_mx4_dequantize(rows, cols, dtype, d_q, d_scales, d_x, as_stream(stream)));
+}
+
+size_t moe_few_workspace_bytes(const moe_shape_t* shape, int32_t form, int32_t shared_F)
+{
+    if (check_few(shape, form, shared_F) != MOE_OK) return 0;
+    return moe::few_ws_layout(*shape, shared_F).total;
+}
+
+moe_status_t moe_few_layer(const moe_shape_t* shape, int32_t form, const void* d_x, const void* d_w_router,
+                           const float* d_bias, const moe_few_weights_t* h_routed, const moe_few_weights_t* h_shared,
+                           int32_t shared_F, void* d_out, int32_t* d_ids, float* d_w, int32_t* d_err, void* d_ws,
+                           size_t ws_bytes, moe_stream_t stream)
+{
+    const moe_status_t st = check_few(shape, form, shared_F);
+    if (st != MOE_OK) return st;
+    const int64_t T = shape->T;
+    if (bad(d_x, T) || bad(d_w_router, 1) || bad_opt(d_bias, 4) || bad_weights(h_routed, form) || bad(d_out, T) ||
+        bad_opt(d_ids, 4) || bad_opt(d_w, 4) || bad(d_err, 1, 4) || bad(d_ws, 1))
+        return MOE_EINVAL;
+    if ((h_shared != nullptr) != (shared_F > 0) || (h_shared && bad_weights(h_shared, form))) return MOE_EINVAL;
+    if (ws_bytes < moe::few_ws_layout(*shape, shared_F).total) return MOE_EINVAL;
+    const MoeFew a{d_x, d_w_router, d_bias, *h_routed, h_shared ? *h_shared : moe_few_weights_t{}, form, shared_F,
+                   d_out, d_ids, d_w, d_err};
+    return dev(moe_launch_few(*shape, a, static_cast<char*>(d_ws), as_stream(stream)));
 }
 
 }  // extern "C"

@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_BF16, MX_BLOCK, Shape, moe_combine, moe_count_plan, moe_gemm_down,
-               moe_gemm_gateup, moe_gemm_schedule, moe_grouped_gemm_mx, moe_grouped_gemm_slots,
+from . import (MOE_BF16, MOE_W_BF16, MOE_W_MX4, MOE_W_MX8, MX_BLOCK, Shape, moe_combine, moe_count_plan,
+               moe_few_layer, moe_few_workspace_bytes, moe_gemm_down, moe_gemm_gateup, moe_gemm_schedule, moe_grouped_gemm_mx, moe_grouped_gemm_slots,
                moe_grouped_gemm_train, moe_mx_workspace_bytes, moe_permute, moe_permute_mx, moe_plan,
                moe_plan_layout, moe_prefetch_replicas, moe_rmsnorm, moe_route, moe_router,
                moe_router_workspace_bytes, moe_workspace_bytes)
@@ -227,3 +227,36 @@ class MoeLayerMx:
                    self.router_ws, st)
         self.experts(self.xq, self.xs, self.ids, self.w, w_gate, w_up, w_down, stream=st)
         return self.out, self.s
+
+
+class MoeLayerFew:
+    """Buffers and the call of a decode step of up to FEW_TOKENS tokens: router,
+    top-k, experts and combine in moe_few_layer.
+
+    A bf16 shape; weights: "bf16", "mx8" or "mx4", the form of every projection;
+    shared_F: width of an always-on shared expert of the same form (None: no shared
+    expert). The buffers belong to one call at a time: calls that may overlap, and
+    captured graphs that may, take an object each.
+    """
+
+    FORMS = {"bf16": MOE_W_BF16, "mx8": MOE_W_MX8, "mx4": MOE_W_MX4}
+
+    def __init__(self, shape: Shape, device="cuda", weights="mx8", shared_F: int | None = None):
+        self.shape, self.form, self.shared_F = shape, self.FORMS[weights], shared_F or 0
+        T, k = shape.T, shape.k
+        need = moe_few_workspace_bytes(shape, self.form, self.shared_F)
+        if need == 0:
+            raise ValueError(f"moe_few_layer has no layer of this shape on {weights} weights")
+        self.out = alloc((T, shape.H), torch.bfloat16, device)
+        self.ids = alloc((T, k), torch.int32, device)
+        self.w = alloc((T, k), torch.float32, device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def forward(self, x, w_router, bias, w_gate, w_up, w_down, shared_w=None, stream=None):
+        """Returns self.out; the router's choice is in self.ids and self.w, and
+        self.err gathers MOE_ERR_NONFINITE from call to call. Weights are (values,
+        scales) pairs, scales None in bfloat16; shared_w: the shared expert's three."""
+        moe_few_layer(self.shape, self.form, x, w_router, bias, w_gate, w_up, w_down, self.out, self.err, self.ws,
+                      shared=shared_w, shared_F=self.shared_F, ids=self.ids, w=self.w, stream=stream)
+        return self.out

@@ -16,23 +16,32 @@ from .block import MX_BLOCK, _bytes, _env, _ptr, _stream
 
 __all__ = [
     "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
-    "moe_mx4_quantize", "moe_mx4_dequantize", "STEP_SYMBOLS",
+    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_few_workspace_bytes", "moe_few_layer", "STEP_SYMBOLS",
+    "MOE_W_BF16", "MOE_W_MX8", "MOE_W_MX4", "FEW_TOKENS",
 ]
 
 #: entry points of include/moe_step.h
 STEP_SYMBOLS = (
     "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
-    "moe_mx4_quantize", "moe_mx4_dequantize",
+    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_few_workspace_bytes", "moe_few_layer",
 )
 
+#: forms of moe_few_layer's weights, and its most tokens
+MOE_W_BF16, MOE_W_MX8, MOE_W_MX4 = 0, 1, 2
+FEW_TOKENS = 32
+
 _VP = ctypes.c_void_p
+
+
+class FewWeightsT(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("gate", "up", "down", "gate_scales", "up_scales", "down_scales")]
 
 
 def signatures():
     """name -> (result type, argument types), for the package's load()."""
     st, sz, i32, i64, f32 = (ctypes.c_int, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64,
                              ctypes.c_float)
-    sp = ctypes.POINTER(_moe.Shape)
+    sp, wp = ctypes.POINTER(_moe.Shape), ctypes.POINTER(FewWeightsT)
     return {
         "moe_block_norm": (st, [sp, _VP, _VP, f32, _VP, _VP, i32, _VP, f32, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
         "moe_block_norm_backward_workspace_bytes": (sz, [sp, i32]),
@@ -40,6 +49,8 @@ def signatures():
                                          _VP, _VP, _VP, sz, _VP]),
         "moe_mx4_quantize": (st, [i64, i64, i32, _VP, _VP, _VP, _VP]),
         "moe_mx4_dequantize": (st, [i64, i64, i32, _VP, _VP, _VP, _VP]),
+        "moe_few_workspace_bytes": (sz, [sp, i32, i32]),
+        "moe_few_layer": (st, [sp, i32, _VP, _VP, _VP, wp, wp, i32, _VP, _VP, _VP, _VP, _VP, sz, _VP]),
     }
 
 
@@ -134,3 +145,40 @@ def moe_mx4_dequantize(q, scales, x, stream=None):
         rows, cols, dtype, _ptr(q, _fours(), "q", n // 2, here), _ptr(scales, stp, "q scales", n // MX_BLOCK, here),
         _ptr(x, acts[_moe.MOE_BF16] + acts[_moe.MOE_F32], "x", 0, here), _stream(stream, here))
     _moe._ok(st, "moe_mx4_dequantize")
+
+
+def moe_few_workspace_bytes(shape, form, shared_F=0) -> int:
+    return int(_moe.load().moe_few_workspace_bytes(ctypes.byref(shape), form, shared_F))
+
+
+def _few_weights(form, projections, n, here, what):
+    """The struct of (values, scales) of gate, up and down, each of n values."""
+    _, acts, ct, stp, _, _ = _env()
+    out = FewWeightsT()
+    for name, (v, s) in zip(("gate", "up", "down"), projections):
+        name_ = f"{what} {name}"
+        if form == MOE_W_BF16:
+            setattr(out, name, _ptr(v, acts[_moe.MOE_BF16], name_, n, here))
+        else:
+            setattr(out, name, _ptr(v, ct if form == MOE_W_MX8 else _fours(), name_, n if form == MOE_W_MX8 else n // 2, here))
+            setattr(out, name + "_scales", _ptr(s, stp, name_ + " scales", n // MX_BLOCK, here))
+    return out
+
+
+def moe_few_layer(shape, form, x, w_router, bias, gate, up, down, out, err, ws, shared=None, shared_F=0, ids=None, w=None,
+                  stream=None):
+    """Router, top-k, experts, shared expert and combine of up to FEW_TOKENS
+    tokens. gate, up, down: (values, scales) of [E][F][H], [E][F][H] and
+    [E][H][F], scales None in bfloat16; shared: the three of one expert of width
+    shared_F; ids and w, the router's choice, may be None."""
+    dev, acts, _, _, f32, i32 = _env()
+    here, T, H, E = dev(), shape.T, shape.H, shape.E
+    bf = acts[_moe.MOE_BF16]
+    routed = _few_weights(form, (gate, up, down), E * shape.F * H, here, "routed")
+    one = None if shared is None else _few_weights(form, shared, shared_F * H, here, "shared")
+    st = _moe.load().moe_few_layer(
+        ctypes.byref(shape), form, _ptr(x, bf, "x", T * H, here), _ptr(w_router, bf, "w_router", E * H, here),
+        _ptr(bias, f32, "bias", E, here, True), ctypes.byref(routed), None if one is None else ctypes.byref(one), shared_F,
+        _ptr(out, bf, "out", T * H, here), _ptr(ids, i32, "ids", shape.N, here, True), _ptr(w, f32, "w", shape.N, here, True),
+        _ptr(err, i32, "err", 1, here), _ptr(ws, None, "ws", 0, here), _bytes(ws), _stream(stream, here))
+    _moe._ok(st, "moe_few_layer")

@@ -9,6 +9,8 @@
  *                             front of the next block
  *   moe_mx4_quantize, moe_mx4_dequantize
  *                             weights in 4-bit blocks
+ *   moe_few_layer             router to combine for a few tokens, on bf16,
+ *                             8-bit or 4-bit weights
  *
  * 4-bit blocks ("mx4"). As the 8-bit blocks of moe_block.h, 32 consecutive
  * values of a row to a scale 2^e stored as the byte e + 127, with e2m1 codes
@@ -100,6 +102,49 @@ moe_status_t moe_mx4_quantize(int64_t rows, int64_t cols, int32_t dtype, const v
  *   dtype[rows][cols] out; limits as moe_mx4_quantize. */
 moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const void *d_q,
                                 const void *d_scales, void *d_x, moe_stream_t stream);
+
+/* Weights of moe_few_layer's experts. MOE_W_BF16: bf16, no scales. MOE_W_MX8,
+ * MOE_W_MX4: codes and scales of 8-bit or 4-bit blocks. */
+typedef enum { MOE_W_BF16 = 0, MOE_W_MX8 = 1, MOE_W_MX4 = 2 } moe_weight_form_t;
+typedef struct moe_few_weights {
+    const void *gate, *up, *down;                      /* [E][F][H], [E][F][H], [E][H][F] */
+    const void *gate_scales, *up_scales, *down_scales; /* of blocks; else not read        */
+} moe_few_weights_t;
+
+/* Most tokens of moe_few_layer. */
+#define MOE_FEW_TOKENS 32
+
+/* Bytes of device workspace moe_few_layer needs (logits, the activations h,
+ * counters, partial sums). shared_F: width of the shared expert, 0 without one. 0 on a
+ * shape that moe_few_layer refuses. Calls that may run at the same time, and
+ * captured graphs that may, need a workspace each. */
+size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t shared_F);
+
+/* The whole layer for T <= MOE_FEW_TOKENS tokens:
+ *   logits = x W_r^T; ids and gate weights w from them as moe_route;
+ *   out[t] = sum_j w[t][j] * W_down[e] (silu(W_gate[e] x_t) * (W_up[e] x_t)),
+ *            e = ids[t][j], in j order of sums in fp32
+ *            (+ the same of the shared expert, weight 1), rounded once to bf16.
+ * Products are of bf16 values (blocks widen to bf16 exactly) with fp32 sums; h
+ * keeps 16 bits of its value (two bf16), so that bf16's rounding of out is the
+ * only one that counts. Each live expert's weights are read once for all of its
+ * tokens. No plan, no dispatch: R and S of the shape are not used.
+ *   shape: dtype MOE_BF16; form a moe_weight_form_t, for the routed and the
+ *   shared experts; MOE_W_MX8 and MOE_W_MX4 need H, F and shared_F multiples
+ *   of 128, MOE_W_BF16 of 64; H <= 8192; else, and for more tokens or another
+ *   dtype, MOE_EUNSUPPORTED;
+ *   d_x bf16[T][H]; d_w_router bf16[E][H]; d_bias float[E] or NULL; h_routed:
+ *   host memory, read before the call returns; h_shared with one expert of
+ *   width shared_F, or NULL with shared_F 0; d_out bf16[T][H]; d_ids
+ *   int32[T][k] and d_w float[T][k], the router's choice, each may be NULL;
+ *   d_err int32[1] in/out (MOE_ERR_NONFINITE: a logit or bias is infinite or
+ *   NaN); d_ws / ws_bytes >= moe_few_workspace_bytes(shape, form, shared_F).
+ * d_out overlaps no input. Calls on the same inputs repeat their bits. */
+moe_status_t moe_few_layer(const moe_shape_t *shape, int32_t form, const void *d_x,
+                           const void *d_w_router, const float *d_bias,
+                           const moe_few_weights_t *h_routed, const moe_few_weights_t *h_shared,
+                           int32_t shared_F, void *d_out, int32_t *d_ids, float *d_w,
+                           int32_t *d_err, void *d_ws, size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

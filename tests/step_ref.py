@@ -147,3 +147,72 @@ def check(got, want, what, t=None):
     off = (got.double() - v).abs()
     bad = ~(off <= tol * (1 + 1e-9) + 1e-300)
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} out, worst {float((off / tol.clamp(min=1e-300)).max()):.3f} of its bound"
+
+
+# ----------------------------------------------------- the layer for a few tokens ----
+
+def whole(w, e):
+    """float64 values of expert e of (values, scales)."""
+    v, s = w
+    if s is None:
+        return v[e].double()
+    if v.dtype == torch.uint8 and v.shape[-1] * 2 == s.shape[-1] * 32:
+        return values4(v[e], s[e])
+    return v[e].view(torch.float8_e4m3fn).double() * torch.exp2(s[e].view(torch.uint8).double() - 127).repeat_interleave(32, -1)
+
+
+def swiglu(x, gate, up, down):
+    """y and its bound for float64 rows x and one expert's float64 weights, products
+    of bf16 values with fp32 sums. A matrix instruction adds 32 products to its sum,
+    off by at most 2^-22 of the magnitudes added; eight waves share K and add up at
+    the end. h is two bf16: 2^-17 of it is lost at most. exp and the quotient are
+    good to 2 ulp, |silu'| <= 1.1."""
+    H, F = gate.shape[1], gate.shape[0]
+    cH, cF = (H / 256 + 12) * 2.0 ** -22, (F / 128 + 24) * 2.0 ** -22
+    g, u = x @ gate.t(), x @ up.t()
+    dg, du = cH * (x.abs() @ gate.abs().t()), cH * (x.abs() @ up.abs().t())
+    silu = g * torch.sigmoid(g)
+    h = silu * u
+    dh = h.abs() * ((g.abs() * 1.5 + 8) * 2.0 ** -23 + 2.0 ** -17) + 1.1 * dg * u.abs() + silu.abs() * du + 1.1 * dg * du
+    return h @ down.t(), dh @ down.abs().t() + cF * ((h.abs() + dh) @ down.abs().t())
+
+
+def logits_of(x, wr):
+    """Router scores and their bound: eight products in turn a chunk of 2048, then
+    tree sums."""
+    z, a = x.double() @ wr.double().t(), x.double().abs() @ wr.double().abs().t()
+    return z, (x.shape[1] / 256 + 8 + 12) * U * a
+
+
+def few(x, wr, bias, ids, gate, up, down, shared=None):
+    """(out, its bound before rounding, w, its bound) for the choice `ids`, and
+    whether ids is a top-k of logits + bias as far as float32 can tell."""
+    z, dz = logits_of(x, wr)
+    score = z if bias is None else z + bias.double()
+    ds = dz + U * score.abs()
+    ids = ids.long()
+    taken = torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids, True)
+    assert bool((taken.sum(-1) == ids.shape[1]).all()), "an expert twice"
+    low = torch.where(taken, score + ds, torch.full_like(score, torch.inf)).amin(-1)
+    high = torch.where(taken, torch.full_like(score, -torch.inf), score - ds).amax(-1)
+    fine = bool((low >= high).all())
+    s, d = score.gather(1, ids), ds.gather(1, ids)
+    fine = fine and bool((s[:, :-1] + d[:, :-1] >= s[:, 1:] - d[:, 1:]).all())
+    l, dl = z.gather(1, ids), dz.gather(1, ids)
+    w = torch.softmax(l, -1)
+    dw = w * (2 * dl.amax(-1, keepdim=True) + 2 * (l - l.amax(-1, keepdim=True)).abs() * 2.0 ** -23 + 12 * U)
+    T, k = ids.shape
+    out = torch.zeros((T, down[0].shape[1]), dtype=torch.float64, device=x.device)
+    tol, mag = torch.zeros_like(out), torch.zeros_like(out)
+    xd = x.double()
+    for e in torch.unique(ids).tolist():
+        tok, j = (ids == e).nonzero(as_tuple=True)
+        y, dy = swiglu(xd[tok], whole(gate, e), whole(up, e), whole(down, e))
+        a, b = w[tok, j][:, None], dw[tok, j][:, None]
+        out.index_add_(0, tok, a * y)
+        tol.index_add_(0, tok, a * dy + b * (y.abs() + dy))
+        mag.index_add_(0, tok, a * y.abs())
+    if shared is not None:
+        y, dy = swiglu(xd, *(whole(m, 0) for m in shared))
+        out, tol, mag = out + y, tol + dy, mag + y.abs()
+    return out, tol + (k + 6) * U * (mag + tol), w, dw, fine

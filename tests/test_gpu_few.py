@@ -1,0 +1,229 @@
+"""GPU parity of moe_few_layer against its plain float64 form (step_ref.py)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import expert_load_balance_amd as moe  # noqa: E402
+from expert_load_balance_amd.layer import MoeLayerFew  # noqa: E402
+
+import step_ref as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV)
+
+
+def blocks(form, w):
+    """(values, scales) of float32 weights in a form, by the library."""
+    if form == "bf16":
+        return w.to(BF), None
+    q = torch.empty(*w.shape[:-1], w.shape[-1] // (1 if form == "mx8" else 2), dtype=torch.uint8, device=DEV)
+    s = torch.empty(*w.shape[:-1], w.shape[-1] // 32, dtype=torch.uint8, device=DEV)
+    (moe.moe_mx_quantize if form == "mx8" else moe.moe_mx4_quantize)(w, q, s)
+    return q, s
+
+
+def layer(case, seed=0):
+    T, H, E, k, F, SF, form = case
+    g = gen(seed + T * 7 + H + E)
+    x = randn(g, T, H).to(BF)
+    wr = (randn(g, E, H) * H ** -0.5).to(BF)
+    bias = randn(g, E) * 0.2
+    w = [blocks(form, randn(g, E, *s) * s[1] ** -0.5) for s in ((F, H), (F, H), (H, F))]
+    shared = [blocks(form, randn(g, 1, *s) * s[1] ** -0.5) for s in ((SF, H), (SF, H), (H, SF))] if SF else None
+    L = MoeLayerFew(moe.Shape(T, H, E, k, F, 1, 0, moe.MOE_BF16), DEV, weights=form, shared_F=SF or None)
+    return L, x, wr, bias, w, shared
+
+
+def check(L, x, wr, bias, w, shared, what):
+    assert int(L.err.item()) == 0
+    out, tol, gates, dw, fine = ref.few(x, wr, bias, L.ids, *w, shared)
+    assert fine, f"{what}: not the k largest scores in order"
+    ref.check(L.w, (gates, dw), f"{what}: gate weights")
+    ref.check(L.out, (out, tol), what, BF)
+
+
+CASES = [
+    # T, H, E, k, F, shared F, form
+    (1, 64, 1, 1, 64, 0, "bf16"), (1, 128, 4, 2, 64, 64, "bf16"), (3, 192, 6, 3, 320, 0, "bf16"),
+    (1, 4096, 128, 8, 1536, 0, "bf16"), (17, 576, 40, 5, 192, 128, "bf16"), (32, 256, 8, 8, 128, 192, "bf16"),
+    (5, 7168, 4, 2, 256, 0, "bf16"), (2, 8192, 3, 2, 128, 0, "bf16"), (4, 1024, 256, 64, 64, 0, "bf16"),
+    (2, 512, 4, 2, 4160, 8256, "bf16"),
+    (1, 128, 4, 1, 128, 0, "mx8"), (2, 4096, 8, 2, 1536, 0, "mx8"), (16, 640, 16, 4, 384, 128, "mx8"),
+    (31, 896, 64, 8, 128, 0, "mx8"), (7, 7168, 6, 3, 256, 256, "mx8"), (3, 8192, 4, 2, 256, 0, "mx8"),
+    (2, 256, 4, 2, 8320, 0, "mx8"),
+    (1, 128, 4, 4, 128, 128, "mx4"), (5, 4096, 8, 2, 768, 0, "mx4"), (16, 7168, 8, 4, 256, 256, "mx4"),
+    (32, 2048, 40, 8, 128, 0, "mx4"), (11, 8192, 4, 2, 384, 0, "mx4"), (1, 1920, 256, 8, 2048, 2048, "mx4"),
+    (3, 384, 4, 2, 14336, 4224, "mx4"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "T%dH%dE%dk%dF%dS%d%s" % c)
+def test_few_layer(case):
+    print("[case] few", case, flush=True)
+    L, x, wr, bias, w, shared = layer(case)
+    ws = L.ws
+    L.ws = torch.full((ws.numel() + 256,), 113, dtype=torch.uint8, device=DEV)[:ws.numel()]   # any contents will do
+    tail = L.ws.as_strided((256,), (1,), ws.numel())
+    for b in (bias, None):
+        L.out.fill_(7.0)
+        L.forward(x, wr, b, *w, shared)
+        torch.cuda.synchronize()
+        check(L, x, wr, b, w, shared, f"{case}")
+        assert bool((tail == 113).all())
+    # the router's choice is optional, and calls repeat their bits
+    out = torch.empty_like(L.out)
+    moe.moe_few_layer(L.shape, L.form, x, wr, None, *w, out, L.err, L.ws, shared=shared, shared_F=L.shared_F)
+    torch.cuda.synchronize()
+    assert torch.equal(out, L.out)
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+@pytest.mark.parametrize("T", [16, 17, 32])
+def test_every_token_on_one_expert(T, form):
+    """Rows of one expert past one tile, the other experts idle."""
+    case = (T, 256, 32, 2, 256, 0, form)
+    L, x, wr, bias, w, shared = layer(case, 5)
+    bias[:] = 0
+    bias[7], bias[30] = 50.0, 60.0
+    L.forward(x, wr, bias, *w)
+    torch.cuda.synchronize()
+    assert L.ids.tolist() == [[30, 7]] * T
+    check(L, x, wr, bias, w, None, f"{case}")
+
+
+def test_ties_go_to_the_lower_expert():
+    """Scores that are equal in every bit: small whole numbers."""
+    T, H, E, k = 5, 64, 200, 7
+    L, x, wr, bias, w, shared = layer((T, H, E, k, 64, 0, "bf16"))
+    g = gen(2)
+    x.copy_(torch.randint(-2, 3, (T, H), generator=g, device=DEV))
+    wr.copy_(torch.randint(-1, 2, (E, H), generator=g, device=DEV))
+    wr[100:] = wr[:100]
+    x[3] = 0                                     # all scores zero, some of them minus zero
+    bias[:] = 0
+    bias[::3] = -0.0
+    L.forward(x, wr, bias, *w)
+    torch.cuda.synchronize()
+    z = x.double() @ wr.double().t()
+    want = torch.sort(z, dim=-1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(L.ids.long(), want) and L.ids[3].tolist() == list(range(k))
+    check(L, x, wr, bias, w, shared, "ties")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_scores_that_are_not_finite_are_told(bad):
+    L, x, wr, bias, w, shared = layer((4, 128, 8, 3, 128, 128, "mx4"))
+    keep = bias[2].item()
+    bias[2] = bad
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    assert int(L.err.item()) == moe.ERR_NONFINITE
+    assert bool(((L.ids >= 0) & (L.ids < 8)).all())
+    L.err.zero_()
+    bias[2] = keep
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    check(L, x, wr, bias, w, shared, "afterwards")
+
+
+def test_a_bad_token_stays_alone():
+    """A NaN in one token's row leaves the other tokens' outputs as they were."""
+    L, x, wr, bias, w, shared = layer((6, 256, 8, 2, 128, 128, "mx8"))
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    want = L.out.clone()
+    x[2, 9] = float("nan")
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    assert int(L.err.item()) == moe.ERR_NONFINITE and bool(torch.isnan(L.out[2]).all())
+    others = [0, 1, 3, 4, 5]
+    assert torch.equal(L.out[others], want[others])
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+def test_calls_beside_each_other_and_from_a_graph(form):
+    """Two layers on two streams at once, each with its own workspace, and a captured
+    one, replayed between them with new tokens."""
+    case = (8, 1024, 32, 4, 512, 256, form)
+    L, x, wr, bias, w, shared = layer(case)
+    A, B, C = (MoeLayerFew(L.shape, DEV, weights=form, shared_F=256) for _ in range(3))
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        C.forward(x, wr, bias, *w, shared)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    g = gen(9)
+    for i in range(4):
+        x.copy_(randn(g, *x.shape))
+        L.forward(x, wr, bias, *w, shared)
+        torch.cuda.synchronize()
+        for o in (A, B, C):
+            o.out.fill_(3.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, o in zip(side, (A, B)):
+                with torch.cuda.stream(s):
+                    o.forward(x, wr, bias, *w, shared)
+            graph.replay()
+        torch.cuda.synchronize()
+        for o in (A, B, C):
+            assert torch.equal(o.out, L.out) and torch.equal(o.ids, L.ids) and int(o.err.item()) == 0, i
+    check(L, x, wr, bias, w, shared, "last")
+
+
+def test_no_tokens():
+    L = MoeLayerFew(moe.Shape(0, 128, 8, 2, 128, 1, 0, moe.MOE_BF16), DEV, weights="mx8")
+    z = torch.zeros(8 * 128 * 128, dtype=torch.uint8, device=DEV)
+    w = (z, z)
+    wr = torch.zeros(8, 128, dtype=BF, device=DEV)
+    assert L.forward(torch.empty(0, 128, dtype=BF, device=DEV), wr, None, w, w, w).shape == (0, 128)
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+def test_a_bad_weight_reaches_its_rows_only(form):
+    """A block that held a NaN: in the down projection one output column of the
+    tokens of that expert, in gate or up all of theirs."""
+    case = (4, 256, 6, 2, 256, 0, form)
+    L, x, wr, bias, w, shared = layer(case)
+    L.forward(x, wr, bias, *w)
+    torch.cuda.synchronize()
+    want, ids = L.out.clone(), L.ids.clone()
+    e = int(ids[0, 0])
+    on = (ids == e).any(-1)
+    for which, row in ((2, 255), (0, 255), (1, 0)):
+        bad = [(v.clone(), s if s is None else s.clone()) for v, s in w]
+        raw = torch.randn(256, 256, device=DEV)
+        raw[row, 250] = float("nan")
+        v, s = blocks(form, raw[None])
+        bad[which][0][e] = v[0]
+        if s is not None:
+            bad[which][1][e] = s[0]
+        raw[row, 250] = 1.0
+        v, s = blocks(form, raw[None])
+        fine = [(v_.clone(), s_ if s_ is None else s_.clone()) for v_, s_ in w]
+        fine[which][0][e] = v[0]
+        if s is not None:
+            fine[which][1][e] = s[0]
+        L.forward(x, wr, bias, *fine)
+        torch.cuda.synchronize()
+        ref_out = L.out.clone()
+        L.forward(x, wr, bias, *bad)
+        torch.cuda.synchronize()
+        assert torch.equal(L.out[~on], want[~on])
+        if which == 2:
+            assert bool(torch.isnan(L.out[on][:, row]).all())
+            keep = [c for c in range(256) if c != row]
+            assert torch.equal(L.out[on][:, keep], ref_out[on][:, keep])
+        else:
+            assert bool(torch.isnan(L.out[on]).all())

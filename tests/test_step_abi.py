@@ -178,3 +178,61 @@ def test_the_backward_form_against_differences(gate_kind, post, pre):
             num[i] = (forward({**p, n: v + e})[0] - forward({**p, n: v - e})[0]) / (2 * h)
         # differences of step h: h^2 of third derivatives, and 2^-52 / h of the loss
         assert torch.allclose(got[names[n]][0].reshape(-1), num, rtol=1e-6, atol=1e-7), n
+
+
+# ------------------------------------------------------- the layer for a few tokens ----
+
+def _few(lib, s, form=1, x=P, wr=P, bias=None, routed=(P,) * 6, shared=None, SF=0, out=P, ids=None, w=None, err=P, ws=P,
+         need=None):
+    from expert_load_balance_amd.step import FewWeightsT
+
+    need = lib.moe_few_workspace_bytes(ctypes.byref(s), form, SF) if need is None else need
+    a = None if routed is None else ctypes.byref(FewWeightsT(*routed))
+    b = None if shared is None else ctypes.byref(FewWeightsT(*shared))
+    return lib.moe_few_layer(ctypes.byref(s), form, x, wr, bias, a, b, SF, out, ids, w, err, ws, need, None)
+
+
+def test_few_layer_refusals(lib):
+    s = moe.Shape(4, 128, 8, 2, 128, 1, 0, moe.MOE_BF16)
+    size = moe.moe_few_workspace_bytes
+    assert size(s, moe.MOE_W_MX8) >= 4 * 8 * 4 + 2 * 8 * 128 * 2 + 8 * 128 * 4
+    assert size(s, moe.MOE_W_MX4, 128) > size(s, moe.MOE_W_MX4)
+    for bad, st in [(s.replace(T=33), EUNSUP), (s.replace(dtype=moe.MOE_F32), EUNSUP), (s.replace(H=192), EUNSUP),
+                    (s.replace(F=192), EUNSUP), (s.replace(H=8320), EUNSUP), (s.replace(E=0), EINVAL),
+                    (s.replace(k=9), EINVAL), (s.replace(T=-1), EINVAL)]:
+        assert size(bad, moe.MOE_W_MX8) == 0
+        assert _few(lib, bad, need=1 << 40) == st, bad
+    assert size(s.replace(H=192, F=192), moe.MOE_W_BF16) > 0
+    assert size(s, 3) == 0 and size(s, -1) == 0 and size(s, 1, -128) == 0 and size(s, 1, 64) == 0
+    assert _few(lib, s, form=3, need=1 << 40) == EINVAL
+    for name in ("x", "wr", "out", "err", "ws", "routed"):
+        assert _few(lib, s, **{name: None}) == EINVAL, name
+    for name in ("x", "wr", "out", "ws"):
+        assert _few(lib, s, **{name: V(4096 + 8)}) == EINVAL, name
+    for name in ("bias", "ids", "w", "err"):
+        assert _few(lib, s, **{name: V(4097)}) == EINVAL, name
+    for i in range(6):
+        for p in (None, V(4104)):
+            w = [P] * 6
+            w[i] = p
+            assert _few(lib, s, routed=w) == EINVAL, i
+            assert _few(lib, s, shared=w, SF=128) == EINVAL, i
+            if i < 3:                                          # (scales are not read in bf16)
+                assert _few(lib, s, form=0, routed=w) == EINVAL, i
+    assert _few(lib, s, shared=(P,) * 6, SF=0) == EINVAL       # a shared expert without a width
+    assert _few(lib, s, SF=128) == EINVAL                      # and the other way round
+    assert _few(lib, s, need=size(s, 1) - 1) == EINVAL
+    assert _few(lib, s.replace(T=0), x=None, out=None) == 0
+
+
+def test_few_layer_wrapper_refuses_what_does_not_fit():
+    torch = pytest.importorskip("torch")
+    from expert_load_balance_amd.layer import MoeLayerFew
+
+    s = moe.Shape(2, 128, 8, 2, 128, 1, 0, moe.MOE_BF16)
+    with pytest.raises(ValueError):
+        MoeLayerFew(s.replace(T=40), "cpu", weights="mx4")
+    L = MoeLayerFew(s, "cpu", weights="mx4")
+    x, w = torch.zeros(2, 128, dtype=torch.bfloat16), (torch.zeros(8, 128, 64, dtype=torch.uint8),) * 2
+    with pytest.raises(ValueError):
+        L.forward(x, torch.zeros(8, 128, dtype=torch.bfloat16), None, w, w, w)
