@@ -54,7 +54,7 @@
 #include <type_traits>
 
 #include "lds_pipe.h"
-#include "mx.h"
+#include "step.h"
 
 namespace {
 
@@ -65,8 +65,6 @@ using moe::mx_rows;
 constexpr int kThreads = 256;
 constexpr int kTN = moe::kMxTileN;
 constexpr int kTK = moe::kMxStage;
-constexpr int kWBytes = kTN * kTK;       // 32 KB of weights per stage
-constexpr int kWCopies = kWBytes / 4096; // 16-byte copies per wave per stage
 constexpr int kSplitRounds = 3;
 constexpr int kNothing = 0x7fffffff;     // stages of the stream past the last unit
 constexpr int kPieces = 4;               // of an expert, loaded ahead of their number
@@ -213,11 +211,22 @@ __device__ __forceinline__ i32x8 frag(const char* p0, const char* p1)
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// A weight operand of 64 values: 8-bit codes as a row's, 4-bit ones in half of
+// the registers.
+template <int WB>
+__device__ __forceinline__ i32x8 wfrag(const char* p0, const char* p1)
+{
+    if constexpr (WB == 8) return frag(p0, p1);
+    const u32x4 a = *reinterpret_cast<const u32x4*>(p0);
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+}
+
 // acc += W T over one 64-value k-step, with the scales in byte B of ws and ts.
-template <int B>
+template <int WB, int B>
 __device__ __forceinline__ f32x16 mfma(const i32x8& w, const i32x8& t, const f32x16& acc, uint32_t ws, uint32_t ts)
 {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, 0, 0, B, (int)ws, B, (int)ts);
+    // (operand formats: 0 is e4m3, 4 is e2m1)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, t, acc, WB == 8 ? 0 : 4, 0, B, (int)ws, B, (int)ts);
 }
 
 // 16 codes to bf16, times their scale (the word's byte B as an exponent):
@@ -236,6 +245,24 @@ __device__ __forceinline__ Bf16x16 widen(const u32x4& c, uint32_t scales)
     for (int i = 0; i < 4; ++i) {
         w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, false));
         w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, true));
+    }
+    return Bf16x16{__builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}),
+                   __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]})};
+}
+
+// The same of 16 codes of 4 bits.
+template <int B>
+__device__ __forceinline__ Bf16x16 widen4(const u32x2& c, uint32_t scales)
+{
+    const uint32_t at = B == 3 ? scales >> 1 : scales << (B == 3 ? 0 : 23 - 8 * B);
+    const float s = __uint_as_float(at & 0x7f800000u);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w[4 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 0));
+        w[4 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 1));
+        w[4 * i + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 2));
+        w[4 * i + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 3));
     }
     return Bf16x16{__builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}),
                    __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]})};
@@ -549,25 +576,29 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
 // smaller kinds, 1 x 4, each all rows x 64 weight rows. WB 32-row weight
 // blocks per wave (gate/up: the first half of them gate, the rest the same
 // columns of up) and TB 32-row token blocks.
-template <int MODE, int KIND>
+template <int MODE, int KIND, int WB>
 struct Geo {
     static constexpr int kRows = mx_rows(KIND);
     static constexpr int WM = KIND == 0 ? 2 : 1, WN = 4 / WM;
-    static constexpr int TB = kRows / 32 / WM, WB = 8 / WN;
+    static constexpr int TB = kRows / 32 / WM, WBL = 8 / WN;
     static constexpr int kA = kRows * kTK;
-    static constexpr int kACopies = kRows / 32;              // per wave per stage
+    static constexpr int kACopies = kRows / 32;              // 16-byte copies per wave per stage
+    static constexpr int kWRow = kTK * WB / 8;               // bytes of a weight row's stage
+    static constexpr int kWBytes = kTN * kWRow;              // 32 or 16 KB of weights per stage
+    static constexpr int kWCopies = kWBytes / 4096, kWBlock = kTN / kWCopies;  // copies, weight rows of one
     static constexpr int kPerStage = kWCopies + kACopies + 2;
     // LDS, kinds 1..3: slots of rows + weights, then their scales, then three
     // row lists. Kind 0: two slots of rows, a ring of 5 weight units of 128
     // rows (a stage takes two), the scales of up to four stages (16 bytes for
     // each weight row, then for each row), the lists.
+    static constexpr int kMostSlots = WB == 8 ? 4 : 7;
     static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
     static constexpr int kScale = (kTN + kRows) * (KIND == 0 ? 16 : 4);
-    static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > 4
-                                                      ? 4 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
+    static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > kMostSlots
+                                                      ? kMostSlots : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
     static constexpr int kAhead = KIND == 0 ? 2 : kSlots - 1;  // stages copied ahead of the products
-    static constexpr int kUnits = KIND == 0 ? 5 : 0, kUnit0 = kSlots * kSlot;
-    static constexpr int kScale0 = kUnit0 + kUnits * 16384;
+    static constexpr int kUnits = KIND == 0 ? 5 : 0, kUnit0 = kSlots * kSlot, kUnit = 128 * kWRow;
+    static constexpr int kScale0 = kUnit0 + kUnits * kUnit;
     static constexpr int kList0 = kScale0 + (KIND == 0 ? 1 : kSlots) * kScale;
     static constexpr int kKept0 = kList0 + 3 * kRows * 4;      // kind 0: three units for each wave
     static constexpr int kBytes = kKept0 + (KIND == 0 ? 4 * 3 * 32 : 0);
@@ -577,19 +608,24 @@ struct Geo {
     // weight-tile row of block j's first row, for wave column wn
     __device__ static int wrow(int wn, int j)
     {
-        return MODE == kGateUp ? (j / (WB / 2)) * 128 + wn * (128 / WN) + (j % (WB / 2)) * 32
+        return MODE == kGateUp ? (j / (WBL / 2)) * 128 + wn * (128 / WN) + (j % (WBL / 2)) * 32
                                : wn * (kTN / WN) + j * 32;
     }
 };
-static_assert(Geo<kGateUp, 0>::kBytes <= 160 * 1024 && Geo<kGateUp, 1>::kBytes <= 160 * 1024 &&
-              Geo<kGateUp, 2>::kBytes <= 160 * 1024 && Geo<kGateUp, 3>::kBytes <= 160 * 1024, "LDS");
 constexpr int max4(int a, int b, int c, int d)
 {
     const int x = a > b ? a : b, y = c > d ? c : d;
     return x > y ? x : y;
 }
-constexpr int kLds = max4(Geo<kGateUp, 0>::kBytes, Geo<kGateUp, 1>::kBytes, Geo<kGateUp, 2>::kBytes,
-                          Geo<kGateUp, 3>::kBytes);
+template <int WB>
+constexpr int kLds = max4(Geo<kGateUp, 0, WB>::kBytes, Geo<kGateUp, 1, WB>::kBytes, Geo<kGateUp, 2, WB>::kBytes,
+                          Geo<kGateUp, 3, WB>::kBytes);
+static_assert(kLds<8> <= 160 * 1024 && kLds<4> <= 160 * 1024, "LDS");
+
+// Place of chunk c (0..3) in a weight row of 64 bytes (4-bit codes): four rows
+// fill the 256 bytes that 16 lanes read at once, so the chunks turn with every
+// fourth row.
+__device__ __forceinline__ int swz4(int r) { return (r >> 2) & 3; }
 
 // Weights that one tile reads are streamed past the caches, those that the
 // expert's other M-tiles read too are kept. Tiles below the launch's whole ones
@@ -611,16 +647,18 @@ enum Weights { kKept, kStreamed, kByExpert };
 // of instructions and the waits count the same.
 //
 // 16-byte copies (see lds_pipe.h): instruction q = wave + 4 i fills rows 8 q
-// .. 8 q + 7 of an operand, lane l row 8 q + l / 8, chunk l % 8. Scales: 4
+// .. 8 q + 7 of an operand, lane l row 8 q + l / 8, chunk l % 8 (4-bit weights:
+// rows 16 q .. 16 q + 15, lane l row 16 q + l / 4, chunk l % 4). Scales: 4
 // bytes (a stage's four blocks) of weight row 64 wave + lane and, in the
 // lanes below kRows / 4, of row kRows / 4 * wave + lane.
-template <int MODE, int KIND, Weights WEIGHTS>
+template <int MODE, int KIND, Weights WEIGHTS, int WB>
 struct Copier {
-    using GE = Geo<MODE, KIND>;
-    const char *ab, *wb0, *wb1, *asb, *sb;  // rows, weight blocks 0..3 and 4..7, scales
-    int upper;                              // down: weight rows from block 4 on (0 or less: none)
+    using GE = Geo<MODE, KIND, WB>;
+    static constexpr int kHalf = GE::kWCopies / 2;  // weight copies of 128 rows
+    const char *ab, *wb0, *wb1, *asb, *sb;  // rows, the first and the other 128 weight rows, scales
+    int upper;                              // down: weight rows from row 128 on (0 or less: none)
     uint32_t aoff[GE::kACopies], woff, asoff, wsoff;
-    int rows32;        // bytes of 32 weight rows
+    int block;         // bytes from a copy's weight rows to the next one's
     int rot, alone;
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
 
@@ -630,12 +668,13 @@ struct Copier {
         const int K = MODE == kGateUp ? g.H : g.F, KS = K / moe::kMxBlock, wrows = MODE == kGateUp ? g.F : g.H;
         const size_t e0 = (size_t)u.e * wrows;
         const size_t x0 = MODE == kGateUp ? 0 : (size_t)u.x0;
-        // (in the down projection's last tile weight blocks 4..7 may lie past
+        // (in the down projection's last tile the other 128 rows may lie past
         // the matrix)
         upper = wrows - u.n0 - kTN / 2;
         ab = uni_ptr((const char*)g.a + x0 * K + u.k0 * kTK);
-        wb0 = uni_ptr((const char*)g.w0 + e0 * K + u.k0 * kTK);
-        wb1 = uni_ptr((const char*)(MODE == kGateUp ? g.w1 : g.w0) + e0 * K + u.k0 * kTK);
+        const int KB = K * WB / 8;
+        wb0 = uni_ptr((const char*)g.w0 + e0 * KB + u.k0 * GE::kWRow);
+        wb1 = uni_ptr((const char*)(MODE == kGateUp ? g.w1 : g.w0) + e0 * KB + u.k0 * GE::kWRow);
         asb = uni_ptr((const char*)g.as + x0 * KS + u.k0 * 4);
         sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + u.k0 * 4);
         st = scalar<0>();
@@ -659,10 +698,10 @@ struct Copier {
             const uint32_t off = source(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16);
             aoff[i] = r < u.rows ? off : kZeroRow;
         }
-        // (blocks of 32 weight rows are 32 K bytes apart)
-        const int r0 = 8 * wave + (lane >> 3);
-        woff = (uint32_t)(u.n0 + r0) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r0)) * 16);
-        rows32 = 32 * K;
+        const int r0 = WB == 8 ? 8 * wave + (lane >> 3) : 16 * wave + (lane >> 2);
+        woff = (uint32_t)(u.n0 + r0) * (uint32_t)KB +
+               (uint32_t)((WB == 8 ? (lane & 7) ^ swz(r0) : (lane & 3) ^ swz4(r0)) * 16);
+        block = GE::kWBlock * KB;
         const int ar = GE::kRows / 4 * wave + lane % (GE::kRows / 4);
         const uint32_t aso = source(ar) * (uint32_t)KS;
         asoff = lane < GE::kRows / 4 && ar < u.rows ? aso : kZeroRow;
@@ -679,31 +718,34 @@ struct Copier {
     // scalar where it is used: a range that came round the loop would be kept
     // in a vector register.
     __device__ __forceinline__ uint32_t range() const { return (KIND == 0 ? KT != kNothing : st < real) ? kCopyRange : 0u; }
+    // Of 4-bit weights the compiler keeps the stage in a vector register.
+    __device__ __forceinline__ static int held(int v) { return WB == 8 ? v : uni(v); }
     // The next stage into a slot; each call of row and weight is one
     // instruction, scales is two.
     __device__ __forceinline__ void row(int i, uint32_t slot, int wave) const
     {
-        copy16(buffer_of(ab, range()), aoff[i], ks() * kTK, slot + wave * 1024 + i * 4096);
+        copy16(buffer_of(ab, range()), aoff[i], held(ks() * kTK), slot + wave * 1024 + i * 4096);
     }
     template <bool STREAM>
-    __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: 32 rows, 4 KB
+    __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: kWBlock rows, 4 KB
     {
-        copy16<STREAM>(buffer_of(i < 4 ? wb0 : wb1, i < 4 || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
-               ks() * kTK + (MODE == kGateUp ? i % 4 : i) * rows32, unit + wave * 1024);
+        const int at = ks() * GE::kWRow + (MODE == kGateUp ? i % kHalf : i) * block;
+        copy16<STREAM>(buffer_of(i < kHalf ? wb0 : wb1, i < kHalf || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
+               held(at), unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
-        copy4(buffer_of(sb, range()), wsoff, ks() * 4, sslot + wave * 256);
-        if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, ks() * 4, sslot + kTN * 4 + wave * GE::kRows);
+        copy4(buffer_of(sb, range()), wsoff, held(ks() * 4), sslot + wave * 256);
+        if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, held(ks() * 4), sslot + kTN * 4 + wave * GE::kRows);
     }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
         if (WEIGHTS == kStreamed || (WEIGHTS == kByExpert && alone)) {
 #pragma unroll
-            for (int i = 0; i < kWCopies; ++i) weight<true>(i, slot + GE::kA + i * 4096, wave);
+            for (int i = 0; i < GE::kWCopies; ++i) weight<true>(i, slot + GE::kA + i * 4096, wave);
         } else {
 #pragma unroll
-            for (int i = 0; i < kWCopies; ++i) weight<false>(i, slot + GE::kA + i * 4096, wave);
+            for (int i = 0; i < GE::kWCopies; ++i) weight<false>(i, slot + GE::kA + i * 4096, wave);
         }
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) row(i, slot, wave);
@@ -726,10 +768,10 @@ __device__ __forceinline__ void copy_list(const Gemm& g, const Unit& u, uint32_t
 // A finished tile: acc[j] of token block i, weight block j.
 template <int MODE, int KIND>
 __device__ __forceinline__ void finish(const Gemm& g, const Unit& u, int i,
-                                       const f32x16 (&acc)[Geo<MODE, KIND>::WB], const int32_t* list,
+                                       const f32x16 (&acc)[Geo<MODE, KIND, 8>::WBL], const int32_t* list,
                                        int wave, int lane)
 {
-    using GE = Geo<MODE, KIND>;
+    using GE = Geo<MODE, KIND, 8>;  // (its waves' blocks are the same for every weight)
     const int fr = lane & 31, half = lane >> 5, wm = wave / GE::WN, wn = wave % GE::WN;
     const int r = (i * GE::WM + wm) * 32 + fr;
     const bool in = r < u.rows;
@@ -738,9 +780,9 @@ __device__ __forceinline__ void finish(const Gemm& g, const Unit& u, int i,
         const auto h = store_to(g.h + (size_t)u.x0 * g.F);
         const auto hs = store_to(g.hs + (size_t)u.x0 * SF);
 #pragma unroll
-        for (int j = 0; j < GE::WB / 2; ++j) {
+        for (int j = 0; j < GE::WBL / 2; ++j) {
             const int col = u.n0 + GE::wrow(wn, j);
-            store_h(acc[j], acc[j + GE::WB / 2], h, in ? (uint32_t)(r * g.F + col + 16 * half) : kZeroRow, hs,
+            store_h(acc[j], acc[j + GE::WBL / 2], h, in ? (uint32_t)(r * g.F + col + 16 * half) : kZeroRow, hs,
                     in ? (uint32_t)(r * SF + col / moe::kMxBlock) : kZeroRow, half);
         }
     } else {
@@ -748,7 +790,7 @@ __device__ __forceinline__ void finish(const Gemm& g, const Unit& u, int i,
         const auto y = store_to(g.y);
         const uint32_t row = (uint32_t)list[in ? r : 0] * (uint32_t)g.H * 2u + 16u * half;
 #pragma unroll
-        for (int j = 0; j < GE::WB; ++j) {
+        for (int j = 0; j < GE::WBL; ++j) {
             const int col = u.n0 + GE::wrow(wn, j);
             store_y(acc[j], y, in && col < g.H ? row + 2u * col : kZeroRow);
         }
@@ -760,19 +802,19 @@ __device__ __forceinline__ void finish(const Gemm& g, const Unit& u, int i,
 template <int MODE, int KIND>
 __device__ __forceinline__ float4* part_at(const Gemm& g, int pidx, int wave, int i, int j, int lane)
 {
-    using GE = Geo<MODE, KIND>;
+    using GE = Geo<MODE, KIND, 8>;
     float* base = g.part[KIND] + (size_t)pidx * GE::kRows * kTN;
-    return reinterpret_cast<float4*>(base) + ((((size_t)wave * GE::TB + i) * GE::WB + j) * 4) * 64 + lane;
+    return reinterpret_cast<float4*>(base) + ((((size_t)wave * GE::TB + i) * GE::WBL + j) * 4) * 64 + lane;
 }
 template <int MODE, int KIND>
 __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
-                                           const f32x16 (&acc)[Geo<MODE, KIND>::WB], int wave, int lane)
+                                           const f32x16 (&acc)[Geo<MODE, KIND, 8>::WBL], int wave, int lane)
 {
-    using GE = Geo<MODE, KIND>;
+    using GE = Geo<MODE, KIND, 8>;
     const bool in = (i * GE::WM + wave / GE::WN) * 32 + (lane & 31) < u.rows;  // padding rows are left out
     const auto to = store_to(part_at<MODE, KIND>(g, u.pidx, wave, i, 0, 0));
 #pragma unroll
-    for (int j = 0; j < GE::WB; ++j)
+    for (int j = 0; j < GE::WBL; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             store16(to, in ? (uint32_t)(((j * 4 + q) * 64 + lane) * 16) : kZeroRow, __float_as_uint(take(acc[j][4 * q])),
@@ -784,10 +826,10 @@ __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
 // Bound by streaming the weights: a ring of up to four stages, one barrier per
 // stage, the fragments read as the products need them. 128 experts of 16 rows
 // of 4096 x 1536: 6.1 TB/s of weights, where a plain read of 4 GB reaches 6.2.
-template <int MODE, int KIND, Weights WEIGHTS>
+template <int MODE, int KIND, Weights WEIGHTS, int WB>
 __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id)
 {
-    using GE = Geo<MODE, KIND>;
+    using GE = Geo<MODE, KIND, WB>;
     // Gate and up of up to 64 rows are multiplied in bf16, which is exact: the
     // 8-bit instruction's cut leaves g and u about 1e-4 off, which sends 0.2 %
     // of h's codes to the other side of their rounding (y is then 0.0024 of its norm
@@ -821,7 +863,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     }
     wait_vm_lgkm<0>();
     slot_barrier();
-    Copier<MODE, KIND, WEIGHTS> cp;
+    Copier<MODE, KIND, WEIGHTS, WB> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0;       // this unit's number
     int at = 0;      // slot of the stage being computed
@@ -880,8 +922,13 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                     const int c = ((2 * B + half) ^ swz(fr)) * 16;
                     Bf16x16 wf[2];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        wf[q] = widen<B>(*reinterpret_cast<const u32x4*>(slot + GE::kA + (GE::wrow(wn, q) + fr) * 128 + c), ws[q]);
+                    for (int q = 0; q < 2; ++q) {
+                        const char* p = slot + GE::kA + (GE::wrow(wn, q) + fr) * GE::kWRow;
+                        if constexpr (WB == 8)
+                            wf[q] = widen<B>(*reinterpret_cast<const u32x4*>(p + c), ws[q]);
+                        else  // block B's 16 bytes, 8 of them per half of the wave
+                            wf[q] = widen4<B>(*reinterpret_cast<const u32x2*>(p + (B ^ swz4(fr)) * 16 + 8 * half), ws[q]);
+                    }
 #pragma unroll
                     for (int b = 0; b < GE::TB; ++b) {
                         const Bf16x16 tf = widen<B>(*reinterpret_cast<const u32x4*>(slot + (32 * b + fr) * 128 + c), ts[b]);
@@ -908,8 +955,9 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                     i32x8 wf[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const char* p = slot + GE::kA + (GE::wrow(wn, q) + fr) * 128;
-                        wf[q] = frag(p + c0, p + c1);
+                        const char* p = slot + GE::kA + (GE::wrow(wn, q) + fr) * GE::kWRow;
+                        if constexpr (WB == 8) wf[q] = wfrag<8>(p + c0, p + c1);
+                        else wf[q] = wfrag<4>(p + ((2 * KK + half) ^ swz4(fr)) * 16, p);
                     }
 #pragma unroll
                     for (int b = 0; b < GE::TB; ++b) {
@@ -917,7 +965,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                         const i32x8 tf = frag(p + c0, p + c1);
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            acc[b][q] = mfma<2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
+                            acc[b][q] = mfma<WB, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
                     }
                 };
                 kstep(std::integral_constant<int, 0>{});
@@ -1001,7 +1049,7 @@ struct ScaleStream {
         n0 = u.n0;
         x0 = MODE == kGateUp ? 0 : u.x0;
         at = u.k0 + u.rot;
-        left = Geo<MODE, 0>::stream_stages(u.KT);
+        left = Geo<MODE, 0, 8>::stream_stages(u.KT);
         const int r = 64 * wave + lane;
         uint32_t off = (MODE == kGateUp ? (uint32_t)list[r] : (uint32_t)r) * (uint32_t)KS;
         asm volatile("" : "+v"(off));  // (as in Copier)
@@ -1031,10 +1079,10 @@ struct ScaleStream {
     }
 };
 
-template <int MODE>
+template <int MODE, int WB>
 __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
 {
-    using GE = Geo<MODE, 0>;
+    using GE = Geo<MODE, 0, WB>;
     const KindWork work = work_of<MODE>(g, 0);
     const int end = work.count;
     // Round r's tile at position p goes to slot p + r: tails lie between whole
@@ -1074,10 +1122,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     }
     wait_vm_lgkm<0>();
     slot_barrier();
-    Copier<MODE, 0, kKept> cp;
+    Copier<MODE, 0, kKept, WB> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0, odd = 0;  // this unit's number; parity of the stage being computed
-    constexpr int kEarly = 4;  // weight copies in a stage's first half (one unit)
+    constexpr int kEarly = GE::kWCopies / 2;  // weight copies in a stage's first half (one unit)
+    constexpr int kLate = GE::kACopies + GE::kWCopies - kEarly;
     // the copies move on to the next unit
     auto follow = [&]() {
         if (cp.st == cp.KT) {
@@ -1090,7 +1139,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     // next one the two after them, and so on
     auto wrap = [&](int x) { return x >= GE::kUnits ? x - GE::kUnits : x; };
     int wat = 0;
-    auto unit_u = [&](int unit, int i) { return lds_u + GE::kUnit0 + (uint32_t)unit * 16384u + (uint32_t)(i % 4) * 4096u; };
+    auto unit_u = [&](int unit, int i) { return lds_u + GE::kUnit0 + (uint32_t)unit * GE::kUnit + (uint32_t)(i % kEarly) * 4096u; };
 
     i32x8 wf[2][4], tf[2][4];
     // Scales of this stage and the rest of its group: the lane's two bytes of
@@ -1099,9 +1148,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     u32x2 ws[4], ts[4];
     // fragment addresses: chunk c of row r is slot chunk c ^ swz(r); of a
     // lane's four chunks (half, half + 2, + 4, + 6) the others differ from
-    // the first in address bits 5 and 6
+    // the first in address bits 5 and 6 (4-bit weights: of two, half and half +
+    // 2, in bit 5)
     const uint32_t fc = (uint32_t)((half ^ swz(fr)) * 16);
-    const uint32_t wfa = (uint32_t)(GE::kUnit0 + (MODE == kGateUp ? wn * 64 : 0) * 128 + fr * 128) + fc;
+    const uint32_t wfa = (uint32_t)(GE::kUnit0 + ((MODE == kGateUp ? wn * 64 : 0) + fr) * GE::kWRow) +
+                         (WB == 8 ? fc : (uint32_t)((half ^ swz4(fr)) * 16));
     const uint32_t tfa = (uint32_t)((wm * 32 + fr) * 128) + fc;
     // fragment id (0..3 weights, 4..7 rows) of the stage in row slot n whose
     // weights start at unit w0 of the ring
@@ -1110,9 +1161,9 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
             // gate/up: blocks 0, 1 in the stage's first unit (gate), 2, 3 in the
             // second; down: all four in unit wn
             const int unit = MODE == kGateUp ? (id < 2 ? w0 : wrap(w0 + 1)) : wn == 0 ? w0 : wrap(w0 + 1);
-            const int o = MODE == kGateUp ? (id % 2) * 4096 : id * 4096;
-            const uint32_t at = (wfa ^ (uint32_t)(64 * kk)) + (uint32_t)unit * 16384u;
-            wf[kk][id] = frag(lds + at + o, lds + (at ^ 32u) + o);
+            const int o = (MODE == kGateUp ? id % 2 : id) * 32 * GE::kWRow;
+            const uint32_t at = (wfa ^ (uint32_t)(GE::kWRow / 2 * kk)) + (uint32_t)unit * GE::kUnit;
+            wf[kk][id] = wfrag<WB>(lds + at + o, lds + (at ^ 32u) + o);
         } else {
             const uint32_t at = (tfa ^ (uint32_t)(64 * kk)) + (uint32_t)n * GE::kSlot;
             const int o = (id - 4) * 8192;
@@ -1167,7 +1218,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
     for (int n = 0; n < 2; ++n) {
         follow();
 #pragma unroll
-        for (int i = 0; i < kWCopies; ++i) cp.template weight<false>(i, unit_u(2 * n + i / 4, i), wave);
+        for (int i = 0; i < GE::kWCopies; ++i) cp.template weight<false>(i, unit_u(2 * n + i / kEarly, i), wave);
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) cp.row(i, slot_u(n), wave);
         ++cp.st;
@@ -1226,7 +1277,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
             const int wnext = wrap(wat + 2), wcopy = wrap(wnext + 2), wcopy1 = wrap(wcopy + 1);
 #pragma unroll
             for (int q = 0; q < kM; ++q) {
-                acc[q >> 2][q & 3] = mfma<0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
+                acc[q >> 2][q & 3] = mfma<WB, 0>(wf[0][q & 3], tf[0][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
                 // this half's share of the reads (NB row blocks) and copies
 #pragma unroll
                 for (int z = 0; z < 4 + NB; ++z)
@@ -1240,11 +1291,11 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
             const uint32_t sl = slot_u(odd);
 #pragma unroll
             for (int q = 0; q < kM; ++q) {
-                acc[q >> 2][q & 3] = mfma<1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
+                acc[q >> 2][q & 3] = mfma<WB, 1>(wf[1][q & 3], tf[1][q >> 2], acc[q >> 2][q & 3], ws[q & 3][0], ts[q >> 2][0]);
 #pragma unroll
-                for (int z = q * 12 / kM; z < (q + 1) * 12 / kM; ++z) {
+                for (int z = q * kLate / kM; z < (q + 1) * kLate / kM; ++z) {
                     if (z < GE::kACopies) cp.row(z, sl, wave);
-                    else if (z - GE::kACopies < kWCopies - kEarly)
+                    else if (z - GE::kACopies < GE::kWCopies - kEarly)
                         cp.template weight<false>(kEarly + z - GE::kACopies, unit_u(wcopy1, z), wave);
                 }
 #pragma unroll
@@ -1287,16 +1338,16 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
 }
 
 // BASE: kind of an expert's whole tiles (mx_base)
-template <int MODE, int BASE>
+template <int MODE, int BASE, int WB>
 __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    __shared__ __attribute__((aligned(1024))) char lds[kLds<WB>];
     const int b = blockIdx.x;
     const int slot_id = b % 8 * (g.P / 8) + b / 8;
-    if constexpr (BASE == 0) big_tiles<MODE>(g, lds);
-    ring_tiles<MODE, 1, BASE == 0 ? kStreamed : kByExpert>(g, lds, slot_id);
-    ring_tiles<MODE, 2, kStreamed>(g, lds, slot_id);
-    ring_tiles<MODE, 3, kStreamed>(g, lds, slot_id);
+    if constexpr (BASE == 0) big_tiles<MODE, WB>(g, lds);
+    ring_tiles<MODE, 1, BASE == 0 ? kStreamed : kByExpert, WB>(g, lds, slot_id);
+    ring_tiles<MODE, 2, kStreamed, WB>(g, lds, slot_id);
+    ring_tiles<MODE, 3, kStreamed, WB>(g, lds, slot_id);
 }
 
 // Whether a launch may cut tiles along K: not where the rows alone make
@@ -1329,7 +1380,7 @@ inline int fix_items(const moe_shape_t& s, int mode, int kind, int P)
 template <int MODE, int KIND>
 __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
 {
-    using GE = Geo<MODE, KIND>;
+    using GE = Geo<MODE, KIND, 8>;
     const KindWork w = work_of<MODE>(g, KIND);
     const int t = item / GE::TB, i = item % GE::TB;
     if (w.S == 1 || t >= w.L) return;
@@ -1338,15 +1389,15 @@ __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
     const int wave = uni((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / GE::WN;
     if ((i * GE::WM + wm) * 32 >= u.rows) return;
-    f32x16 acc[GE::WB];
+    f32x16 acc[GE::WBL];
 #pragma unroll
-    for (int j = 0; j < GE::WB; ++j)
+    for (int j = 0; j < GE::WBL; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
     const int last = (i * GE::WM + wm) * 32 + (lane & 31) < u.rows ? w.S : 0;  // padding rows have no parts
     for (int p = 0; p < last; ++p)
 #pragma unroll
-        for (int j = 0; j < GE::WB; ++j) {
+        for (int j = 0; j < GE::WBL; ++j) {
             const float4* src = part_at<MODE, KIND>(g, p * w.L + t, wave, i, j, lane);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1401,11 +1452,9 @@ int persistent_grid()
     return grid;
 }
 
-}  // namespace
-
-hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const void* a_s,
-                                      const int32_t* plan, const MoeMxWeights& w, void* y,
-                                      char* ws, hipStream_t st)
+template <int WB>
+hipError_t launch(const moe_shape_t& s, const void* a, const void* a_s, const int32_t* plan, const MoeMxWeights& w,
+                  void* y, char* ws, hipStream_t st)
 {
     const int N = s.T * s.k, base = moe::mx_base(s);
     if (N == 0) return hipSuccess;
@@ -1434,7 +1483,7 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.s0 = w.gate_s;
     g.w1 = w.up;
     g.s1 = w.up_s;
-    (base == 0 ? gemm_mx_kernel<kGateUp, 0> : gemm_mx_kernel<kGateUp, 1>)<<<g.P, kThreads, 0, st>>>(g);
+    (base == 0 ? gemm_mx_kernel<kGateUp, 0, WB> : gemm_mx_kernel<kGateUp, 1, WB>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_fixup<kGateUp>(g, s, st)) != hipSuccess) return e;
     g.ntn = (s.H + kTN - 1) / kTN;
@@ -1444,7 +1493,23 @@ hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const
     g.w0 = w.down;
     g.s0 = w.down_s;
     g.w1 = g.s1 = nullptr;
-    (base == 0 ? gemm_mx_kernel<kDown, 0> : gemm_mx_kernel<kDown, 1>)<<<g.P, kThreads, 0, st>>>(g);
+    (base == 0 ? gemm_mx_kernel<kDown, 0, WB> : gemm_mx_kernel<kDown, 1, WB>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     return launch_fixup<kDown>(g, s, st);
+}
+
+}  // namespace
+
+hipError_t moe_launch_grouped_gemm_mx(const moe_shape_t& s, const void* a, const void* a_s,
+                                      const int32_t* plan, const MoeMxWeights& w, void* y,
+                                      char* ws, hipStream_t st)
+{
+    return launch<8>(s, a, a_s, plan, w, y, ws, st);
+}
+
+hipError_t moe_launch_grouped_gemm_mx4(const moe_shape_t& s, const void* a, const void* a_s,
+                                       const int32_t* plan, const MoeMxWeights& w, void* y,
+                                       char* ws, hipStream_t st)
+{
+    return launch<4>(s, a, a_s, plan, w, y, ws, st);
 }

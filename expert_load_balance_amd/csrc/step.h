@@ -113,6 +113,9 @@ hipError_t moe_launch_mx4_quantize(int64_t rows, int64_t cols, int dtype, const 
                                    void* scales, hipStream_t st);
 hipError_t moe_launch_mx4_dequantize(int64_t rows, int64_t cols, int dtype, const void* q,
                                      const void* scales, void* x, hipStream_t st);
+hipError_t moe_launch_grouped_gemm_mx4(const moe_shape_t& s, const void* a, const void* a_s,
+                                       const int32_t* plan, const MoeMxWeights& w, void* y,
+                                       char* ws, hipStream_t st);
 
 // --------------------------------------------- the layer for a few tokens --
 namespace moe {

@@ -34,6 +34,13 @@ moe_status_t check_blocks(int64_t rows, int64_t cols, int32_t dtype, const void*
     return bad(x, rows) || bad(q, rows) || bad(scales, rows) ? MOE_EINVAL : MOE_OK;
 }
 
+moe_status_t check_mx(const moe_shape_t* s)
+{
+    const moe_status_t st = moe_check_shape(s);
+    if (st != MOE_OK) return st;
+    return s->dtype != MOE_BF16 || s->H % 128 || s->F % 128 ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
 moe_status_t check_few(const moe_shape_t* s, int32_t form, int32_t shared_F)
 {
     const moe_status_t st = moe_check_shape(s);
@@ -126,6 +133,30 @@ moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const
     const moe_status_t st = check_blocks(rows, cols, dtype, d_x, d_q, d_scales);
     if (st != MOE_OK) return st;
     return dev(moe_launch_mx4_dequantize(rows, cols, dtype, d_q, d_scales, d_x, as_stream(stream)));
+}
+
+size_t moe_mx4_workspace_bytes(const moe_shape_t* shape)
+{
+    return check_mx(shape) == MOE_OK ? moe::mx_ws_layout(*shape).total : 0;
+}
+
+moe_status_t moe_grouped_gemm_mx4(const moe_shape_t* shape, const void* d_a, const void* d_a_scales,
+                                  const int32_t* d_plan, const void* d_w_gate, const void* d_gate_scales,
+                                  const void* d_w_up, const void* d_up_scales, const void* d_w_down,
+                                  const void* d_down_scales, void* d_y, void* d_ws, size_t ws_bytes, moe_stream_t stream)
+{
+    const moe_status_t st = check_mx(shape);
+    if (st != MOE_OK) return st;
+    const int64_t T = shape->T;
+    if (bad(d_a, T) || bad(d_a_scales, T) || bad(d_plan, 1, 4) || bad(d_w_gate, 1) || bad(d_gate_scales, 1) ||
+        bad(d_w_up, 1) || bad(d_up_scales, 1) || bad(d_w_down, 1) || bad(d_down_scales, 1) || bad(d_y, T) || bad(d_ws, 1))
+        return MOE_EINVAL;
+    if (ws_bytes < moe::mx_ws_layout(*shape).total) return MOE_EINVAL;
+    const MoeMxWeights w{static_cast<const uint8_t*>(d_w_gate), static_cast<const uint8_t*>(d_gate_scales),
+                         static_cast<const uint8_t*>(d_w_up), static_cast<const uint8_t*>(d_up_scales),
+                         static_cast<const uint8_t*>(d_w_down), static_cast<const uint8_t*>(d_down_scales)};
+    return dev(moe_launch_grouped_gemm_mx4(*shape, d_a, d_a_scales, d_plan, w, d_y, static_cast<char*>(d_ws),
+                                           as_stream(stream)));
 }
 
 size_t moe_few_workspace_bytes(const moe_shape_t* shape, int32_t form, int32_t shared_F)

@@ -10,8 +10,9 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_BF16, MOE_W_BF16, MOE_W_MX4, MOE_W_MX8, MX_BLOCK, Shape, moe_combine, moe_count_plan,
-               moe_few_layer, moe_few_workspace_bytes, moe_gemm_down, moe_gemm_gateup, moe_gemm_schedule, moe_grouped_gemm_mx, moe_grouped_gemm_slots,
-               moe_grouped_gemm_train, moe_mx_workspace_bytes, moe_permute, moe_permute_mx, moe_plan,
+               moe_few_layer, moe_few_workspace_bytes, moe_gemm_down, moe_gemm_gateup, moe_gemm_schedule, moe_grouped_gemm_mx, moe_grouped_gemm_mx4,
+               moe_grouped_gemm_slots,
+               moe_grouped_gemm_train, moe_mx4_workspace_bytes, moe_mx_workspace_bytes, moe_permute, moe_permute_mx, moe_plan,
                moe_plan_layout, moe_prefetch_replicas, moe_rmsnorm, moe_route, moe_router,
                moe_router_workspace_bytes, moe_workspace_bytes)
 
@@ -159,14 +160,17 @@ class MoeLayerMx:
     addition), router, and the experts in 8-bit blocks.
 
     A shape whose dtype is MOE_BF16 with H and F multiples of 128. Weights are
-    (codes, scales) pairs as moe_mx_quantize makes them. The buffers belong to
+    (codes, scales) pairs as moe_mx_quantize makes them, or, with weight_bits 4, as
+    moe_mx4_quantize does (rows and activations stay in 8 bits). The buffers belong to
     one call at a time: calls that may overlap take an object each. A layer with a
     shared expert makes forward's calls itself and hands that expert's rows, made
     from self.xn, to experts.
     """
 
-    def __init__(self, shape: Shape, device="cuda"):
-        self.shape = shape
+    def __init__(self, shape: Shape, device="cuda", weight_bits: int = 8):
+        if weight_bits not in (4, 8):
+            raise ValueError(f"weights of {weight_bits} bits: 8 or 4")
+        self.shape, self.weight_bits = shape, weight_bits
         T, H, E, k, R = shape.T, shape.H, shape.E, shape.k, shape.R
         N, i32, u8, f32 = T * k, torch.int32, torch.uint8, torch.float32
         self.s = alloc((T, H), torch.bfloat16, device)
@@ -196,10 +200,10 @@ class MoeLayerMx:
         # count needs only the head of it, but its size is one per shape
         self.ws = bytes_(moe_workspace_bytes(shape))
         self.router_ws = bytes_(moe_router_workspace_bytes(shape))
-        self.mx_ws = bytes_(moe_mx_workspace_bytes(shape))
+        self.mx_ws = bytes_((moe_mx_workspace_bytes if weight_bits == 8 else moe_mx4_workspace_bytes)(shape))
 
     def experts(self, xq, xs, ids, w, w_gate, w_up, w_down, shared_y=None, stream=None):
-        """Count + plan, dispatch, the 8-bit grouped GEMM and the combine, from
+        """Count + plan, dispatch, the grouped GEMM on blocks and the combine, from
         the 8-bit rows and the router's choice (ids, gate weights w) to
         self.out."""
         s, st = self.shape, stream if stream is not None else torch.cuda.current_stream()
@@ -208,8 +212,8 @@ class MoeLayerMx:
                        self.ws, self.plan, st)
         moe_permute_mx(s, xq, xs, ids, self.eidx, self.plan, self.buf_q, self.buf_s, self.dest_row,
                        self.row_src, st)
-        moe_grouped_gemm_mx(s, self.buf_q, self.buf_s, self.plan, w_gate, w_up, w_down, self.y,
-                            self.mx_ws, st)
+        gemm = moe_grouped_gemm_mx if self.weight_bits == 8 else moe_grouped_gemm_mx4
+        gemm(s, self.buf_q, self.buf_s, self.plan, w_gate, w_up, w_down, self.y, self.mx_ws, st)
         moe_combine(s, self.y, self.dest_row, w, shared_y, self.out, st)
         return self.out
 

@@ -16,14 +16,16 @@ from .block import MX_BLOCK, _bytes, _env, _ptr, _stream
 
 __all__ = [
     "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
-    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_few_workspace_bytes", "moe_few_layer", "STEP_SYMBOLS",
+    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_workspace_bytes", "moe_grouped_gemm_mx4",
+    "moe_few_workspace_bytes", "moe_few_layer", "STEP_SYMBOLS",
     "MOE_W_BF16", "MOE_W_MX8", "MOE_W_MX4", "FEW_TOKENS",
 ]
 
 #: entry points of include/moe_step.h
 STEP_SYMBOLS = (
     "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
-    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_few_workspace_bytes", "moe_few_layer",
+    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_workspace_bytes", "moe_grouped_gemm_mx4",
+    "moe_few_workspace_bytes", "moe_few_layer",
 )
 
 #: forms of moe_few_layer's weights, and its most tokens
@@ -49,6 +51,8 @@ def signatures():
                                          _VP, _VP, _VP, sz, _VP]),
         "moe_mx4_quantize": (st, [i64, i64, i32, _VP, _VP, _VP, _VP]),
         "moe_mx4_dequantize": (st, [i64, i64, i32, _VP, _VP, _VP, _VP]),
+        "moe_mx4_workspace_bytes": (sz, [sp]),
+        "moe_grouped_gemm_mx4": (st, [sp, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, sz, _VP]),
         "moe_few_workspace_bytes": (sz, [sp, i32, i32]),
         "moe_few_layer": (st, [sp, i32, _VP, _VP, _VP, wp, wp, i32, _VP, _VP, _VP, _VP, _VP, sz, _VP]),
     }
@@ -145,6 +149,26 @@ def moe_mx4_dequantize(q, scales, x, stream=None):
         rows, cols, dtype, _ptr(q, _fours(), "q", n // 2, here), _ptr(scales, stp, "q scales", n // MX_BLOCK, here),
         _ptr(x, acts[_moe.MOE_BF16] + acts[_moe.MOE_F32], "x", 0, here), _stream(stream, here))
     _moe._ok(st, "moe_mx4_dequantize")
+
+
+def moe_mx4_workspace_bytes(shape) -> int:
+    return int(_moe.load().moe_mx4_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_grouped_gemm_mx4(shape, a, a_scales, plan, w_gate, w_up, w_down, y, ws, stream=None):
+    """moe_grouped_gemm_mx with weights in 4-bit blocks. w_gate, w_up, w_down:
+    (codes, scales) of [E][F][H], [E][F][H] and [E][H][F] values; y bfloat16 [N][H]."""
+    dev, acts, ct, stp, _, i32 = _env()
+    here, N, H = dev(), shape.N, shape.H
+    n, four = shape.E * shape.F * H, _fours()
+    w = []
+    for name, (q, s) in zip(("w_gate", "w_up", "w_down"), (w_gate, w_up, w_down)):
+        w += [_ptr(q, four, name, n // 2, here), _ptr(s, stp, name + " scales", n // MX_BLOCK, here)]
+    st = _moe.load().moe_grouped_gemm_mx4(
+        ctypes.byref(shape), _ptr(a, ct, "a", N * H, here), _ptr(a_scales, stp, "a scales", N * H // MX_BLOCK, here),
+        _ptr(plan, i32, "plan", _moe.plan_layout_total(shape), here), *w,
+        _ptr(y, acts[_moe.MOE_BF16], "y", N * H, here), _ptr(ws, None, "ws", 0, here), _bytes(ws), _stream(stream, here))
+    _moe._ok(st, "moe_grouped_gemm_mx4")
 
 
 def moe_few_workspace_bytes(shape, form, shared_F=0) -> int:

@@ -7,8 +7,9 @@
  *                             stream: the norm behind a block, its gate, the
  *                             residual's scale and addition, and the norm in
  *                             front of the next block
- *   moe_mx4_quantize, moe_mx4_dequantize
- *                             weights in 4-bit blocks
+ *   moe_mx4_quantize, moe_mx4_dequantize, moe_grouped_gemm_mx4
+ *                             weights in 4-bit blocks, and the routed experts
+ *                             on them (serving)
  *   moe_few_layer             router to combine for a few tokens, on bf16,
  *                             8-bit or 4-bit weights
  *
@@ -102,6 +103,26 @@ moe_status_t moe_mx4_quantize(int64_t rows, int64_t cols, int32_t dtype, const v
  *   dtype[rows][cols] out; limits as moe_mx4_quantize. */
 moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const void *d_q,
                                 const void *d_scales, void *d_x, moe_stream_t stream);
+
+/* Bytes of device workspace moe_grouped_gemm_mx4 needs. 0 on a shape that is
+ * bad or no 8-bit shape (moe_permute_mx). Calls that may run at the same time,
+ * and captured graphs that may, need a workspace each. */
+size_t moe_mx4_workspace_bytes(const moe_shape_t *shape);
+
+/* moe_grouped_gemm_mx with weights in 4-bit blocks: rows and h stay in 8-bit
+ * blocks, the products are the scaled matrix instructions' of 4-bit by 8-bit
+ * codes, with their precision as described there.
+ *   d_a, d_a_scales uint8[N][H], uint8[N][H/32] (moe_permute_mx's buffer);
+ *   d_w_gate, d_w_up uint8[E][F][H/2] with scales uint8[E][F][H/32];
+ *   d_w_down uint8[E][H][F/2] with scales uint8[E][H][F/32]; d_plan from
+ *   moe_plan; d_y bf16[N][H] out; d_ws / ws_bytes >=
+ *   moe_mx4_workspace_bytes(shape). Rows do not mix: a NaN stays in its row. */
+moe_status_t moe_grouped_gemm_mx4(const moe_shape_t *shape, const void *d_a, const void *d_a_scales,
+                                  const int32_t *d_plan, const void *d_w_gate,
+                                  const void *d_gate_scales, const void *d_w_up,
+                                  const void *d_up_scales, const void *d_w_down,
+                                  const void *d_down_scales, void *d_y, void *d_ws, size_t ws_bytes,
+                                  moe_stream_t stream);
 
 /* Weights of moe_few_layer's experts. MOE_W_BF16: bf16, no scales. MOE_W_MX8,
  * MOE_W_MX4: codes and scales of 8-bit or 4-bit blocks. */

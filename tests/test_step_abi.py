@@ -236,3 +236,21 @@ def test_few_layer_wrapper_refuses_what_does_not_fit():
     x, w = torch.zeros(2, 128, dtype=torch.bfloat16), (torch.zeros(8, 128, 64, dtype=torch.uint8),) * 2
     with pytest.raises(ValueError):
         L.forward(x, torch.zeros(8, 128, dtype=torch.bfloat16), None, w, w, w)
+
+
+def test_grouped_gemm_mx4_refusals(lib):
+    s = moe.Shape(16, 128, 8, 2, 128, 4, 2, moe.MOE_BF16)
+    need = moe.moe_mx4_workspace_bytes(s)
+    assert need >= 32 * 128 + 32 * 4
+    assert moe.moe_mx4_workspace_bytes(s.replace(H=192)) == 0 and moe.moe_mx4_workspace_bytes(s.replace(R=3)) == 0
+    g = lib.moe_grouped_gemm_mx4
+    for i in range(11):
+        a = [P] * 11
+        a[i] = None
+        assert g(ctypes.byref(s), *a, need, None) == EINVAL, i
+        if i != 2:                                            # (the plan is int32: 4-byte aligned)
+            a[i] = V(4096 + 8)
+            assert g(ctypes.byref(s), *a, need, None) == EINVAL, i
+    assert g(ctypes.byref(s), *[P] * 11, need - 1, None) == EINVAL
+    assert g(ctypes.byref(s.replace(H=64)), *[P] * 11, need, None) == EUNSUP
+    assert g(ctypes.byref(s.replace(dtype=moe.MOE_F32)), *[P] * 11, need, None) == EUNSUP
