@@ -250,24 +250,6 @@ __device__ __forceinline__ Bf16x16 widen(const u32x4& c, uint32_t scales)
                    __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]})};
 }
 
-// The same of 16 codes of 4 bits.
-template <int B>
-__device__ __forceinline__ Bf16x16 widen4(const u32x2& c, uint32_t scales)
-{
-    const uint32_t at = B == 3 ? scales >> 1 : scales << (B == 3 ? 0 : 23 - 8 * B);
-    const float s = __uint_as_float(at & 0x7f800000u);
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        w[4 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 0));
-        w[4 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 1));
-        w[4 * i + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 2));
-        w[4 * i + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 3));
-    }
-    return Bf16x16{__builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}),
-                   __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]})};
-}
-
 // (a, b) -> lanes 0..31: (a, a of the lane 32 up); lanes 32..63: (b of the
 // lane 32 down, b).
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
@@ -418,8 +400,19 @@ struct Unit {
     int alone;             // the expert has no other M-tile
 };
 
+// Stages that K values take: of 128 values, and in the small tiles of 4-bit
+// weights of 256, so that a stage takes whole 128-byte lines of every weight row
+// (the last one may be half). With 64 bytes of a row a stage and the copies
+// streamed, a line was fetched again for its other half: 256 tokens of 128 experts of
+// 4096 x 1536, gate/up 251 us, down 139.
+template <int KIND, int WB>
+__device__ __forceinline__ int stages(int K)
+{
+    return WB == 4 && KIND > 0 ? (K + 2 * kTK - 1) / (2 * kTK) : K / kTK;
+}
+
 struct Gemm {
-    int E, ntn, H, F, P;
+    int E, ntn, H, F, P, N;
     int split;                  // tiles may be cut along K
     const uint8_t *a, *as;
     const int32_t *sched, *vrow;
@@ -446,10 +439,10 @@ __device__ __forceinline__ Gemm again()
 }
 
 // The units of kinds 0 .. KIND - 1 come first.
-template <int MODE>
+template <int MODE, int WB>
 __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 {
-    const int KT = (MODE == kGateUp ? g.H : g.F) / kTK;
+    const int K = MODE == kGateUp ? g.H : g.F;
     KindWork w{0, 0, 1, 0, 0, 0};
     int n[kMxKinds], total = 0, first = 0;
 #pragma unroll
@@ -457,7 +450,7 @@ __device__ __forceinline__ KindWork work_of(const Gemm& g, int kind)
 #pragma unroll
     for (int k = 0; k < kMxKinds; ++k)
         if (k <= kind) {
-            w = kind_work(n[k], first, g.P, KT, g.split && total < kSplitRounds * g.P, k > 0, total - n[0]);
+            w = kind_work(n[k], first, g.P, k == 0 ? stages<0, WB>(K) : stages<1, WB>(K), g.split && total < kSplitRounds * g.P, k > 0, total - n[0]);
             first += w.count;
         }
     return w;
@@ -533,13 +526,13 @@ __device__ __forceinline__ void tile_by_wave(const Gemm& g, int t, Unit& u)
     place<MODE, KIND>(g, t, 64 * chunk + at, of(a), of(b), of(c), of(d), u);
 }
 
-template <int MODE, int KIND, bool WAVE = false>
+template <int MODE, int KIND, int WB, bool WAVE = false>
 __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
 {
     Unit u;
     int t = j - w.first;
     u.k0 = 0;
-    u.KT = (MODE == kGateUp ? g.H : g.F) / kTK;
+    u.KT = stages<KIND, WB>(MODE == kGateUp ? g.H : g.F);
     u.pidx = -1;
     int half = -1;
     if (KIND == 0 && w.halves && t >= w.full) {
@@ -581,9 +574,10 @@ struct Geo {
     static constexpr int kRows = mx_rows(KIND);
     static constexpr int WM = KIND == 0 ? 2 : 1, WN = 4 / WM;
     static constexpr int TB = kRows / 32 / WM, WBL = 8 / WN;
-    static constexpr int kA = kRows * kTK;
-    static constexpr int kACopies = kRows / 32;              // 16-byte copies per wave per stage
-    static constexpr int kWRow = kTK * WB / 8;               // bytes of a weight row's stage
+    static constexpr int kPanels = WB == 4 && KIND > 0 ? 2 : 1;  // of 128 values of K in a stage, rows by panel
+    static constexpr int kA = kRows * kTK * kPanels;
+    static constexpr int kACopies = kRows / 32 * kPanels;    // 16-byte copies per wave per stage
+    static constexpr int kWRow = kTK * kPanels * WB / 8;     // bytes of a weight row's stage
     static constexpr int kWBytes = kTN * kWRow;              // 32 or 16 KB of weights per stage
     static constexpr int kWCopies = kWBytes / 4096, kWBlock = kTN / kWCopies;  // copies, weight rows of one
     static constexpr int kPerStage = kWCopies + kACopies + 2;
@@ -591,11 +585,13 @@ struct Geo {
     // row lists. Kind 0: two slots of rows, a ring of 5 weight units of 128
     // rows (a stage takes two), the scales of up to four stages (16 bytes for
     // each weight row, then for each row), the lists.
-    static constexpr int kMostSlots = WB == 8 ? 4 : 7;
+    // (The scales of a stage of 256 values come as 16 bytes a row, with those of
+    // its neighbour: one copy instruction costs as much for 4 bytes a row.)
     static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
-    static constexpr int kScale = (kTN + kRows) * (KIND == 0 ? 16 : 4);
-    static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > kMostSlots
-                                                      ? kMostSlots : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
+    static constexpr int kScaleRow = KIND == 0 || kPanels == 2 ? 16 : 4;
+    static constexpr int kScale = (kTN + kRows) * kScaleRow;
+    static constexpr int kSlots = KIND == 0 ? 2 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale) > 4
+                                                      ? 4 : (160 * 1024 - 3 * kRows * 4) / (kSlot + kScale);
     static constexpr int kAhead = KIND == 0 ? 2 : kSlots - 1;  // stages copied ahead of the products
     static constexpr int kUnits = KIND == 0 ? 5 : 0, kUnit0 = kSlots * kSlot, kUnit = 128 * kWRow;
     static constexpr int kScale0 = kUnit0 + kUnits * kUnit;
@@ -622,9 +618,9 @@ constexpr int kLds = max4(Geo<kGateUp, 0, WB>::kBytes, Geo<kGateUp, 1, WB>::kByt
                           Geo<kGateUp, 3, WB>::kBytes);
 static_assert(kLds<8> <= 160 * 1024 && kLds<4> <= 160 * 1024, "LDS");
 
-// Place of chunk c (0..3) in a weight row of 64 bytes (4-bit codes): four rows
-// fill the 256 bytes that 16 lanes read at once, so the chunks turn with every
-// fourth row.
+// Place of chunk c (0..3) in a weight row of 64 bytes (4-bit codes, 256-row
+// tiles): four rows fill the 256 bytes that 16 lanes read at once, so the chunks
+// turn with every fourth row.
 __device__ __forceinline__ int swz4(int r) { return (r >> 2) & 3; }
 
 // Weights that one tile reads are streamed past the caches, those that the
@@ -647,8 +643,8 @@ enum Weights { kKept, kStreamed, kByExpert };
 // of instructions and the waits count the same.
 //
 // 16-byte copies (see lds_pipe.h): instruction q = wave + 4 i fills rows 8 q
-// .. 8 q + 7 of an operand, lane l row 8 q + l / 8, chunk l % 8 (4-bit weights:
-// rows 16 q .. 16 q + 15, lane l row 16 q + l / 4, chunk l % 4). Scales: 4
+// .. 8 q + 7 of an operand, lane l row 8 q + l / 8, chunk l % 8 (of weight rows
+// of 64 bytes rows 16 q .. 16 q + 15, lane l row 16 q + l / 4, chunk l % 4). Scales: 4
 // bytes (a stage's four blocks) of weight row 64 wave + lane and, in the
 // lanes below kRows / 4, of row kRows / 4 * wave + lane.
 template <int MODE, int KIND, Weights WEIGHTS, int WB>
@@ -661,6 +657,9 @@ struct Copier {
     int block;         // bytes from a copy's weight rows to the next one's
     int rot, alone;
     int st, KT, real;  // the next stage to copy, the unit's stages in the stream, those with data
+    int k0, half;      // 4-bit small tiles: the unit's first stage, its stage of 128 values only (or -1)
+    uint32_t whalf;    // and woff without that stage's second half
+    uint32_t arange, wrange;  // bytes of the rows' and of the expert's scales
 
     // list: the unit's row list in LDS (gate/up; down reads h in virtual order)
     __device__ __forceinline__ void setup(const Gemm& g, const Unit& u, const int32_t* list, int wave, int lane)
@@ -671,12 +670,20 @@ struct Copier {
         // (in the down projection's last tile the other 128 rows may lie past
         // the matrix)
         upper = wrows - u.n0 - kTN / 2;
-        ab = uni_ptr((const char*)g.a + x0 * K + u.k0 * kTK);
-        const int KB = K * WB / 8;
+        ab = uni_ptr((const char*)g.a + x0 * K + u.k0 * (kTK * GE::kPanels));
+        const int KB = K * WB / 8;  // bytes of a weight row
         wb0 = uni_ptr((const char*)g.w0 + e0 * KB + u.k0 * GE::kWRow);
         wb1 = uni_ptr((const char*)(MODE == kGateUp ? g.w1 : g.w0) + e0 * KB + u.k0 * GE::kWRow);
-        asb = uni_ptr((const char*)g.as + x0 * KS + u.k0 * 4);
-        sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + u.k0 * 4);
+        const int s0 = GE::kPanels == 1 ? u.k0 * 4 : 0;
+        asb = uni_ptr((const char*)g.as + x0 * KS + s0);
+        sb = uni_ptr((const char*)(MODE == kGateUp && wave >= 2 ? g.s1 : g.s0) + e0 * KS + s0);
+        if constexpr (GE::kPanels == 2) {
+            k0 = u.k0;
+            half = K % (2 * kTK) ? stages<KIND, WB>(K) - 1 - u.k0 : -1;
+            // (a group of 16 bytes may reach past a row's end, and the last row's past the array)
+            arange = uni((int)((uint32_t)(g.N - (int)x0) * (uint32_t)KS));
+            wrange = uni((int)((uint32_t)wrows * (uint32_t)KS));
+        }
         st = scalar<0>();
         rot = u.rot;
         if (WEIGHTS == kByExpert) alone = u.alone;
@@ -694,13 +701,14 @@ struct Copier {
         };
 #pragma unroll
         for (int i = 0; i < GE::kACopies; ++i) {
-            const int r = 8 * (wave + 4 * i) + (lane >> 3);
+            const int r = 8 * (wave + 4 * (i % (GE::kRows / 32))) + (lane >> 3);
             const uint32_t off = source(r) * (uint32_t)K + (uint32_t)(((lane & 7) ^ swz(r)) * 16);
             aoff[i] = r < u.rows ? off : kZeroRow;
         }
-        const int r0 = WB == 8 ? 8 * wave + (lane >> 3) : 16 * wave + (lane >> 2);
-        woff = (uint32_t)(u.n0 + r0) * (uint32_t)KB +
-               (uint32_t)((WB == 8 ? (lane & 7) ^ swz(r0) : (lane & 3) ^ swz4(r0)) * 16);
+        const int r0 = GE::kWRow == 128 ? 8 * wave + (lane >> 3) : 16 * wave + (lane >> 2);
+        const int chunk = GE::kWRow == 128 ? (lane & 7) ^ swz(r0) : (lane & 3) ^ swz4(r0);
+        woff = (uint32_t)(u.n0 + r0) * (uint32_t)KB + (uint32_t)(chunk * 16);
+        if constexpr (GE::kPanels == 2) whalf = chunk < 4 ? woff : kZeroRow;
         block = GE::kWBlock * KB;
         const int ar = GE::kRows / 4 * wave + lane % (GE::kRows / 4);
         const uint32_t aso = source(ar) * (uint32_t)KS;
@@ -724,19 +732,34 @@ struct Copier {
     // instruction, scales is two.
     __device__ __forceinline__ void row(int i, uint32_t slot, int wave) const
     {
-        copy16(buffer_of(ab, range()), aoff[i], held(ks() * kTK), slot + wave * 1024 + i * 4096);
+        if constexpr (GE::kPanels == 1) {
+            copy16(buffer_of(ab, range()), aoff[i], held(ks() * kTK), slot + wave * 1024 + i * 4096);
+        } else {
+            const int panel = i / (GE::kRows / 32);
+            copy16(buffer_of(ab, panel && ks() == half ? 0u : range()), aoff[i], held((2 * ks() + panel) * kTK),
+                   slot + wave * 1024 + i * 4096);
+        }
     }
     template <bool STREAM>
     __device__ __forceinline__ void weight(int i, uint32_t unit, int wave) const  // unit: kWBlock rows, 4 KB
     {
         const int at = ks() * GE::kWRow + (MODE == kGateUp ? i % kHalf : i) * block;
-        copy16<STREAM>(buffer_of(i < kHalf ? wb0 : wb1, i < kHalf || MODE == kGateUp || upper > 0 ? range() : 0u), woff,
+        uint32_t off = woff;
+        if constexpr (GE::kPanels == 2) off = ks() == half ? whalf : woff;
+        copy16<STREAM>(buffer_of(i < kHalf ? wb0 : wb1, i < kHalf || MODE == kGateUp || upper > 0 ? range() : 0u), off,
                held(at), unit + wave * 1024);
     }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
-        copy4(buffer_of(sb, range()), wsoff, held(ks() * 4), sslot + wave * 256);
-        if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, held(ks() * 4), sslot + kTN * 4 + wave * GE::kRows);
+        if constexpr (GE::kPanels == 1) {
+            copy4(buffer_of(sb, range()), wsoff, ks() * 4, sslot + wave * 256);
+            if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, ks() * 4, sslot + kTN * 4 + wave * GE::kRows);
+        } else {  // 512 values' worth, of which the stage's are the first or the second half
+            const int at = held((k0 + ks()) / 2 * 16);
+            copy16(buffer_of(sb, st < real ? wrange : 0u), wsoff, at, sslot + wave * 1024);
+            if (lane < GE::kRows / 4)
+                copy16(buffer_of(asb, st < real ? arange : 0u), asoff, at, sslot + kTN * 16 + wave * GE::kRows * 4);
+        }
     }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
@@ -838,8 +861,10 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // would: 256 x 128 rows of 7168 x 2048 1585 -> 2423 us. The down projection's
     // cut reaches y without a rounding in between, and exact products there
     // would take 1 % on 32-row tiles and 10 % on 64 (256 x 64 rows: 748 -> 827 us).
-    constexpr bool kWide = MODE == kGateUp && KIND >= 2;
-    const KindWork work = work_of<MODE>(g, KIND);
+    // 4-bit weights stream in half the time, and there the slower products would
+    // show: 128 x 16 rows of 4096 x 1536 164 -> 203 us.
+    constexpr bool kWide = WB == 8 && MODE == kGateUp && KIND >= 2;
+    const KindWork work = work_of<MODE, WB>(g, KIND);
     const int end = work.first + work.count, P = g.P;
     // this workgroup's first unit of the kind
     int j = work.first + uni((slot_id - work.first % g.P + g.P) % g.P);
@@ -854,11 +879,11 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // what the previous kind left in flight has landed, in every wave
     wait_vm_lgkm<0>();
     slot_barrier();
-    Unit u = unit_of<MODE, KIND, true>(g, work, j), un = u;
+    Unit u = unit_of<MODE, KIND, WB, true>(g, work, j), un = u;
     copy_list<KIND>(g, u, list_u(0), wave, lane);
     bool more = j + g.P < end;
     if (more) {
-        un = unit_of<MODE, KIND, true>(g, work, j + g.P);
+        un = unit_of<MODE, KIND, WB, true>(g, work, j + g.P);
         copy_list<KIND>(g, un, list_u(1), wave, lane);
     }
     wait_vm_lgkm<0>();
@@ -889,6 +914,15 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
         Unit u2 = un;
         bool more2 = false;
         const int KT = GE::stream_stages(u.KT);
+        int cut = -1;  // the stage of 128 values only, in the order of the stages computed
+        if constexpr (GE::kPanels == 2) {
+            const Gemm ga = again();
+            const int K = MODE == kGateUp ? ga.H : ga.F;
+            if (K % (2 * kTK)) {
+                cut = stages<KIND, WB>(K) - 1 - u.k0 - u.rot;
+                cut = uni(cut < 0 ? cut + u.KT : cut);
+            }
+        }
         for (int s = 0; s < KT; ++s) {
             // this stage landed in this wave: the copies of the kAhead - 1
             // stages after it may be out (a list or stores among them only
@@ -903,7 +937,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                 more2 = j + 2 * P < end;
                 if (more2) {
                     const Gemm ga = again();
-                    u2 = unit_of<MODE, KIND>(ga, work, j + 2 * P);
+                    u2 = unit_of<MODE, KIND, WB>(ga, work, j + 2 * P);
                     copy_list<KIND>(ga, u2, list_u(m + 2), wave, lane);
                 }
             }
@@ -911,65 +945,76 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
             const char* slot = lds + at * GE::kSlot;
             const char* ssl = lds + GE::kScale0 + at * GE::kScale;
             at = at + 1 == GE::kSlots ? 0 : at + 1;
-            uint32_t ws[2], ts[GE::TB];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) ws[q] = *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * 4);
+            for (int p = 0; p < GE::kPanels; ++p) {
+                // 128 values of K: the four blocks' scales of each weight and row
+                const int so = GE::kPanels == 1 ? 0 : ((u.k0 + s) & 1) * 8 + 4 * p;
+                const char *const rows = slot + p * (GE::kRows * kTK), *const weights = slot + GE::kA;
+                uint32_t ws[2], ts[GE::TB];
 #pragma unroll
-            for (int b = 0; b < GE::TB; ++b) ts[b] = *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * 4);
-            if constexpr (kWide) {
-                auto block = [&](auto b_tag) {  // 32 values of K, 16 per half of the wave
-                    constexpr int B = decltype(b_tag)::value;
-                    const int c = ((2 * B + half) ^ swz(fr)) * 16;
-                    Bf16x16 wf[2];
+                for (int q = 0; q < 2; ++q)
+                    ws[q] = *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * GE::kScaleRow + so);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const char* p = slot + GE::kA + (GE::wrow(wn, q) + fr) * GE::kWRow;
-                        if constexpr (WB == 8)
-                            wf[q] = widen<B>(*reinterpret_cast<const u32x4*>(p + c), ws[q]);
-                        else  // block B's 16 bytes, 8 of them per half of the wave
-                            wf[q] = widen4<B>(*reinterpret_cast<const u32x2*>(p + (B ^ swz4(fr)) * 16 + 8 * half), ws[q]);
-                    }
+                for (int b = 0; b < GE::TB; ++b)
+                    ts[b] = *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * GE::kScaleRow + so);
+                if (GE::kPanels == 2 && p == 1) {
+                    // (past a row's end the scales are the next row's, maybe NaN, on codes of 0)
+                    const uint32_t keep = s == cut ? 0u : ~0u;
 #pragma unroll
-                    for (int b = 0; b < GE::TB; ++b) {
-                        const Bf16x16 tf = widen<B>(*reinterpret_cast<const u32x4*>(slot + (32 * b + fr) * 128 + c), ts[b]);
+                    for (int q = 0; q < 2; ++q) ws[q] &= keep;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            acc[b][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[q].lo, tf.lo, acc[b][q], 0, 0, 0);
-                            acc[b][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[q].hi, tf.hi, acc[b][q], 0, 0, 0);
-                        }
-                    }
-                };
-                block(std::integral_constant<int, 0>{});
-                block(std::integral_constant<int, 1>{});
-                block(std::integral_constant<int, 2>{});
-                block(std::integral_constant<int, 3>{});
-            } else {
-                // this lane's blocks: bytes 0 and 2 of the word, 1 and 3 in the upper lanes
-#pragma unroll
-                for (int q = 0; q < 2; ++q) ws[q] >>= 8 * half;
-#pragma unroll
-                for (int b = 0; b < GE::TB; ++b) ts[b] >>= 8 * half;
-                auto kstep = [&](auto kk_tag) {
-                    constexpr int KK = decltype(kk_tag)::value;
-                    const int c0 = ((4 * KK + half) ^ swz(fr)) * 16, c1 = ((4 * KK + 2 + half) ^ swz(fr)) * 16;
-                    i32x8 wf[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const char* p = slot + GE::kA + (GE::wrow(wn, q) + fr) * GE::kWRow;
-                        if constexpr (WB == 8) wf[q] = wfrag<8>(p + c0, p + c1);
-                        else wf[q] = wfrag<4>(p + ((2 * KK + half) ^ swz4(fr)) * 16, p);
-                    }
-#pragma unroll
-                    for (int b = 0; b < GE::TB; ++b) {
-                        const char* p = slot + (32 * b + fr) * 128;
-                        const i32x8 tf = frag(p + c0, p + c1);
+                    for (int b = 0; b < GE::TB; ++b) ts[b] &= keep;
+                }
+                if constexpr (kWide) {
+                    auto block = [&](auto b_tag) {  // 32 values of K, 16 per half of the wave
+                        constexpr int B = decltype(b_tag)::value;
+                        const int c = ((2 * B + half) ^ swz(fr)) * 16;
+                        Bf16x16 wf[2];
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            acc[b][q] = mfma<WB, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
-                    }
-                };
-                kstep(std::integral_constant<int, 0>{});
-                kstep(std::integral_constant<int, 1>{});
+                            wf[q] = widen<B>(*reinterpret_cast<const u32x4*>(weights + (GE::wrow(wn, q) + fr) * GE::kWRow + c), ws[q]);
+#pragma unroll
+                        for (int b = 0; b < GE::TB; ++b) {
+                            const Bf16x16 tf = widen<B>(*reinterpret_cast<const u32x4*>(rows + (32 * b + fr) * 128 + c), ts[b]);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                acc[b][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[q].lo, tf.lo, acc[b][q], 0, 0, 0);
+                                acc[b][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[q].hi, tf.hi, acc[b][q], 0, 0, 0);
+                            }
+                        }
+                    };
+                    block(std::integral_constant<int, 0>{});
+                    block(std::integral_constant<int, 1>{});
+                    block(std::integral_constant<int, 2>{});
+                    block(std::integral_constant<int, 3>{});
+                } else {
+                    // this lane's blocks: bytes 0 and 2 of the word, 1 and 3 in the upper lanes
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) ws[q] >>= 8 * half;
+#pragma unroll
+                    for (int b = 0; b < GE::TB; ++b) ts[b] >>= 8 * half;
+                    auto kstep = [&](auto kk_tag) {
+                        constexpr int KK = decltype(kk_tag)::value;
+                        const int c0 = ((4 * KK + half) ^ swz(fr)) * 16, c1 = ((4 * KK + 2 + half) ^ swz(fr)) * 16;
+                        i32x8 wf[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const char* w = weights + (GE::wrow(wn, q) + fr) * GE::kWRow;
+                            if constexpr (WB == 8) wf[q] = wfrag<8>(w + c0, w + c1);
+                            else wf[q] = wfrag<4>(w + ((4 * p + 2 * KK + half) ^ swz(fr)) * 16, w);
+                        }
+#pragma unroll
+                        for (int b = 0; b < GE::TB; ++b) {
+                            const char* t = rows + (32 * b + fr) * 128;
+                            const i32x8 tf = frag(t + c0, t + c1);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                acc[b][q] = mfma<WB, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
+                        }
+                    };
+                    kstep(std::integral_constant<int, 0>{});
+                    kstep(std::integral_constant<int, 1>{});
+                }
             }
         }
         drain();
@@ -1083,7 +1128,7 @@ template <int MODE, int WB>
 __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
 {
     using GE = Geo<MODE, 0, WB>;
-    const KindWork work = work_of<MODE>(g, 0);
+    const KindWork work = work_of<MODE, WB>(g, 0);
     const int end = work.count;
     // Round r's tile at position p goes to slot p + r: tails lie between whole
     // tiles at regular distances, and no slot should get only the one or the
@@ -1113,10 +1158,10 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
         const int4 a = p[0], b = p[1];
         return Unit{uni(a.x), uni(a.y), uni(a.z), uni(a.w), uni(b.x), uni(b.y), uni(b.z), uni(b.w), 0};
     };
-    Unit u = unit_of<MODE, 0, true>(g, work, unit_at(g, 0));
+    Unit u = unit_of<MODE, 0, WB, true>(g, work, unit_at(g, 0));
     copy_list<0>(g, u, list_u(0), wave, lane);
     if (units > 1) {
-        const Unit un = unit_of<MODE, 0, true>(g, work, unit_at(g, 1));
+        const Unit un = unit_of<MODE, 0, WB, true>(g, work, unit_at(g, 1));
         keep(1, un);
         copy_list<0>(g, un, list_u(1), wave, lane);
     }
@@ -1255,7 +1300,7 @@ __device__ __forceinline__ void big_tiles(const Gemm& g, char* lds)
                 // before stage 0's barrier
                 if (m + 2 < units) {
                     const Gemm ga = again();
-                    const Unit u2 = unit_of<MODE, 0>(ga, work_of<MODE>(ga, 0), unit_at(ga, m + 2));
+                    const Unit u2 = unit_of<MODE, 0, WB>(ga, work_of<MODE, WB>(ga, 0), unit_at(ga, m + 2));
                     keep(m + 2, u2);
                     copy_list<0>(ga, u2, list_u(m + 2), wave, opaque_v(lane));
                 }
@@ -1377,11 +1422,11 @@ inline int fix_items(const moe_shape_t& s, int mode, int kind, int P)
     return (int)(tiles < P ? tiles : P) * tb;
 }
 
-template <int MODE, int KIND>
+template <int MODE, int KIND, int WB>
 __device__ __forceinline__ void fix_tile(const Gemm& g, int item)
 {
     using GE = Geo<MODE, KIND, 8>;
-    const KindWork w = work_of<MODE>(g, KIND);
+    const KindWork w = work_of<MODE, WB>(g, KIND);
     const int t = item / GE::TB, i = item % GE::TB;
     if (w.S == 1 || t >= w.L) return;
     Unit u;
@@ -1415,17 +1460,17 @@ struct FixGrid {
     int end[kMxKinds];
 };
 
-template <int MODE>
+template <int MODE, int WB>
 __global__ __launch_bounds__(kThreads) void mx_fixup_kernel(const Gemm g, const FixGrid f)
 {
     const int b = blockIdx.x;
-    if (b < f.end[0]) fix_tile<MODE, 0>(g, b);
-    else if (b < f.end[1]) fix_tile<MODE, 1>(g, b - f.end[0]);
-    else if (b < f.end[2]) fix_tile<MODE, 2>(g, b - f.end[1]);
-    else fix_tile<MODE, 3>(g, b - f.end[2]);
+    if (b < f.end[0]) fix_tile<MODE, 0, WB>(g, b);
+    else if (b < f.end[1]) fix_tile<MODE, 1, WB>(g, b - f.end[0]);
+    else if (b < f.end[2]) fix_tile<MODE, 2, WB>(g, b - f.end[1]);
+    else fix_tile<MODE, 3, WB>(g, b - f.end[2]);
 }
 
-template <int MODE>
+template <int MODE, int WB>
 hipError_t launch_fixup(const Gemm& g, const moe_shape_t& s, hipStream_t st)
 {
     if (!g.split) return hipSuccess;
@@ -1433,7 +1478,7 @@ hipError_t launch_fixup(const Gemm& g, const moe_shape_t& s, hipStream_t st)
     int n = 0;
     for (int k = 0; k < kMxKinds; ++k) f.end[k] = n += fix_items(s, MODE, k, g.P);
     if (n == 0) return hipSuccess;
-    mx_fixup_kernel<MODE><<<n, kThreads, 0, st>>>(g, f);
+    mx_fixup_kernel<MODE, WB><<<n, kThreads, 0, st>>>(g, f);
     return hipGetLastError();
 }
 
@@ -1469,6 +1514,7 @@ hipError_t launch(const moe_shape_t& s, const void* a, const void* a_s, const in
     g.H = s.H;
     g.F = s.F;
     g.P = persistent_grid();
+    g.N = N;
     g.sched = sched;
     g.vrow = vrow;
     g.h = reinterpret_cast<uint8_t*>(ws + W.h);
@@ -1485,7 +1531,7 @@ hipError_t launch(const moe_shape_t& s, const void* a, const void* a_s, const in
     g.s1 = w.up_s;
     (base == 0 ? gemm_mx_kernel<kGateUp, 0, WB> : gemm_mx_kernel<kGateUp, 1, WB>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_fixup<kGateUp>(g, s, st)) != hipSuccess) return e;
+    if ((e = launch_fixup<kGateUp, WB>(g, s, st)) != hipSuccess) return e;
     g.ntn = (s.H + kTN - 1) / kTN;
     g.split = may_split(s, kDown, g.P);
     g.a = g.h;
@@ -1495,7 +1541,7 @@ hipError_t launch(const moe_shape_t& s, const void* a, const void* a_s, const in
     g.w1 = g.s1 = nullptr;
     (base == 0 ? gemm_mx_kernel<kDown, 0, WB> : gemm_mx_kernel<kDown, 1, WB>)<<<g.P, kThreads, 0, st>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_fixup<kDown>(g, s, st);
+    return launch_fixup<kDown, WB>(g, s, st);
 }
 
 }  // namespace

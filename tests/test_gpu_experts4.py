@@ -118,6 +118,25 @@ def test_float4_tensors_and_refusals():
         MoeLayerMx(shape, DEV, weight_bits=6)
 
 
+@pytest.mark.parametrize("H,F", [(640, 1152), (128, 384), (1152, 512)])
+def test_a_nan_block_of_a_weight_stays_in_its_column(H, F):
+    """The first block of a row of W_down, next to the end of the row before it."""
+    T, E, k = 40, 2, 1
+    g = gen(H + F)
+    L = MoeLayerMx(moe.Shape(T, H, E, k, F, 1, 0, moe.MOE_BF16), DEV, weight_bits=4)
+    xq, xs = quantized(randn(g, T, H))
+    ids, w = choose(g, T, E, k, 0.0)
+    wts = weights4(g, E, F, H)
+    run(L, xq, xs, ids, w, wts)
+    check(L, xq, xs, ids, wts)
+    want, on = L.out.clone(), ids[:, 0] == 0
+    wts[2][1][0, 70, 0] = 255
+    run(L, xq, xs, ids, w, wts)
+    cols = [c for c in range(H) if c != 70]
+    assert bool(torch.isnan(L.out[on][:, 70]).all())
+    assert torch.equal(L.out[on][:, cols], want[on][:, cols]) and torch.equal(L.out[~on], want[~on])
+
+
 @pytest.mark.parametrize("T", [3, 700])
 def test_experts_mx4_from_a_graph_beside_eager_calls(T):
     H, E, k, F = 512, 8, 2, 512
