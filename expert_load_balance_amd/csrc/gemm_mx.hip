@@ -250,6 +250,13 @@ __device__ __forceinline__ Bf16x16 widen(const u32x4& c, uint32_t scales)
                    __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]})};
 }
 
+// The codes of a word whose exponent is 8 and more (of 15), the others 0. The
+// byte masks are the top exponent bits, spread by the permute's sign selectors.
+__device__ __forceinline__ uint32_t upper_codes(uint32_t v)
+{
+    return v & __builtin_amdgcn_perm(v << 9, v << 1, 0x090b080au);
+}
+
 // (a, b) -> lanes 0..31: (a, a of the lane 32 up); lanes 32..63: (b of the
 // lane 32 down, b).
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
@@ -861,9 +868,12 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // would: 256 x 128 rows of 7168 x 2048 1585 -> 2423 us. The down projection's
     // cut reaches y without a rounding in between, and exact products there
     // would take 1 % on 32-row tiles and 10 % on 64 (256 x 64 rows: 748 -> 827 us).
-    // 4-bit weights stream in half the time, and there the slower products would
-    // show: 128 x 16 rows of 4096 x 1536 164 -> 203 us.
-    constexpr bool kWide = WB == 8 && MODE == kGateUp && KIND >= 2;
+    // With 4-bit weights the rows' codes are multiplied in two parts instead, those
+    // of exponent 8 and more and the others: the products of a part differ by 10
+    // binades at most, of which the cut takes 9. The time for a stage is half, and
+    // the widening's conversions would show: 128 x 16 rows of 4096 x 1536, gate/up
+    // 164 us in one part, 203 in bf16.
+    constexpr bool kWide = WB == 8 && MODE == kGateUp && KIND >= 2, kSplit = WB == 4 && MODE == kGateUp && KIND >= 2;
     const KindWork work = work_of<MODE, WB>(g, KIND);
     const int end = work.first + work.count, P = g.P;
     // this workgroup's first unit of the kind
@@ -1006,10 +1016,21 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 #pragma unroll
                         for (int b = 0; b < GE::TB; ++b) {
                             const char* t = rows + (32 * b + fr) * 128;
-                            const i32x8 tf = frag(t + c0, t + c1);
+                            i32x8 tf = frag(t + c0, t + c1), low;
+                            if constexpr (kSplit)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int up = (int)upper_codes((uint32_t)tf[i]);
+                                    low[i] = tf[i] ^ up;
+                                    tf[i] = up;
+                                }
 #pragma unroll
                             for (int q = 0; q < 2; ++q)
                                 acc[b][q] = mfma<WB, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
+                            if constexpr (kSplit)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q)
+                                    acc[b][q] = mfma<WB, 2 * KK>(wf[q], low, acc[b][q], ws[q], ts[b]);
                         }
                     };
                     kstep(std::integral_constant<int, 0>{});
