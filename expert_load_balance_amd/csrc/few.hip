@@ -221,8 +221,9 @@ __device__ void choose(const Few& f, Tables& s, bool tell)
 
 // --------------------------------------------------------------- the forms --
 // A unit of K: kLoads loads of 16 bytes a lane, each kSub operands of 32 values
-// (8 a lane). Lane (r, g) = (lane % 16, lane / 16) holds row r, and of load q's
-// values those from q * 4 * kSub * 8 + g * kSub * 8 on.
+// (8 a lane). Lane (r, g) = (lane % 16, lane / 16) holds row r, and of the unit the
+// values of bytes (g * kLoads + q) * 16 on in load q: both loads of a 128-byte unit
+// touch the whole line.
 template <int FORM>
 struct Form;
 template <>
@@ -243,12 +244,12 @@ struct Form<MOE_W_MX4> {
 
 // One load's operands. scales: the row's four scale bytes of the unit.
 template <int FORM>
-__device__ __forceinline__ void widen(const u32x4& c, uint32_t scales, int q, int g, bf16x8 (&o)[Form<FORM>::kSub])
+__device__ __forceinline__ void widen(const u32x4& c, uint32_t scales, int g, bf16x8 (&o)[Form<FORM>::kSub])
 {
     if constexpr (FORM == MOE_W_BF16) {
         o[0] = __builtin_bit_cast(bf16x8, c);
     } else {
-        const uint32_t byte = (scales >> (8 * (FORM == MOE_W_MX8 ? 2 * q + (g >> 1) : g))) & 255u;
+        const uint32_t byte = (scales >> (8 * g)) & 255u;
         const float s = __uint_as_float(byte << 23);
 #pragma unroll
         for (int j = 0; j < Form<FORM>::kSub; ++j) {
@@ -283,6 +284,29 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* base, uint32_t records, u
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 2));
 }
 
+// N words (1, 2, 3 or 4) a lane, kept in the caches. No more than are used: a word of
+// a load in flight that nobody reads is a free register to the compiler, which then
+// waits for every load before it takes it.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* base, uint32_t records, uint32_t voff, uint32_t soff, uint32_t* w)
+{
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)records, 0x00020000);
+    if constexpr (N == 1) {
+        w[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0);
+    } else if constexpr (N == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)voff, (int)soff, 0));
+        w[0] = v[0], w[1] = v[1];
+    } else if constexpr (N == 3) {
+        const u32x3 v = __builtin_bit_cast(u32x3, __builtin_amdgcn_raw_buffer_load_b96(r, (int)voff, (int)soff, 0));
+        w[0] = v[0], w[1] = v[1], w[2] = v[2];
+    } else {
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
+        w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+    }
+}
+
 // The waves' sums of one step, [wave][stream][lane], doubled.
 struct Reduce {
     f32x4 v[2][kWaves][2][64];
@@ -303,34 +327,41 @@ __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const ui
     constexpr int L = 2 * NU * FM::kLoads, D0 = ring_of(L), U = D0 > L ? D0 / L : 1, D = D0 > L ? U * L : D0;
     static_assert(L % D == 0 || D % L == 0, "ring");
     constexpr bool kScaled = FORM != MOE_W_BF16;
-    constexpr int kSL = (NU + 3) / 4;  // 16-byte loads of a row's scales
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const uint32_t row_bytes = (uint32_t)FM::bytes(K);
-    const uint32_t voff = (uint32_t)r * row_bytes + (uint32_t)u0 * FM::kUnitBytes + 16u * g;
+    const uint32_t voff = (uint32_t)r * row_bytes + (uint32_t)u0 * FM::kUnitBytes + 16u * FM::kLoads * g;
     const uint32_t step_bytes = (uint32_t)step_rows * row_bytes, bytes = (uint32_t)rows * row_bytes;
     const uint32_t srow = (uint32_t)(K / 32), svoff = (uint32_t)r * srow + 4u * u0, sstep = (uint32_t)step_rows * srow;
     const uint8_t* const wp[2] = {uni_ptr(w[0]), uni_ptr(w[1])};
     const uint8_t* const sp[2] = {uni_ptr(sc[0]), uni_ptr(sc[1])};
 
-    u32x4 ring[D], next[U][2][kSL];
+    u32x4 ring[D];
+    uint32_t next[U][2][NU];
     // load i of the step `ahead` from s on, into its place in the ring
     auto issue = [&](int place, int s, int ahead, int i) {
         const int u = i / 2 / FM::kLoads, q = i / 2 % FM::kLoads;
         ring[place] = load16(wp[i % 2], s + ahead < s1 && u < cnt ? bytes : 0u, voff,
-                             (uint32_t)(s + ahead) * step_bytes + u * FM::kUnitBytes + q * 64);
+                             (uint32_t)(s + ahead) * step_bytes + u * FM::kUnitBytes + q * 16);
     };
     auto scales = [&](int place, int s) {
         if constexpr (kScaled)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < kSL; ++i)
-                    next[place][m][i] = load16(sp[m], s < s1 ? (uint32_t)rows * srow : 0u, svoff, (uint32_t)s * sstep + 16 * i);
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t records = s < s1 ? (uint32_t)rows * srow : 0u, at = (uint32_t)s * sstep;
+                load_words<(NU < 4 ? NU : 4)>(sp[m], records, svoff, at, next[place][m]);
+                if constexpr (NU > 4) load_words<NU - 4>(sp[m], records, svoff, at + 16, next[place][m] + 4);
+            }
     };
+    // (the barriers keep the loads in this order among the products: moved behind
+    // them, each wait would be for all of them)
 #pragma unroll
     for (int k = 0; k < U; ++k) scales(k, s0 + k);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < D; ++i) issue(i, s0, i / L, i % L);
+    for (int i = 0; i < D; ++i) {
+        issue(i, s0, i / L, i % L);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     for (int s = s0; s < s1; s += U) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -340,20 +371,22 @@ __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const ui
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < NU; ++i) cur[m][i] = i < cnt ? next[k][m][i / 4][i % 4] : 0u;  // (past cnt: other rows')
+                    for (int i = 0; i < NU; ++i) cur[m][i] = i < cnt ? next[k][m][i] : 0u;  // (past cnt: other rows')
                 scales(k, s + k + U);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const int m = i % 2, u = i / 2 / FM::kLoads, q = i / 2 % FM::kLoads;
                 bf16x8 a[FM::kSub];
-                widen<FORM>(ring[(k * L + i) % D], kScaled ? cur[m][u] : 0u, q, g, a);
+                widen<FORM>(ring[(k * L + i) % D], kScaled ? cur[m][u] : 0u, g, a);
 #pragma unroll
                 for (int j = 0; j < FM::kSub; ++j)
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
                         acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[n][(u * FM::kLoads + q) * FM::kSub + j], acc[m], 0, 0, 0);
                 issue((k * L + i) % D, s, k + (i + D) / L, (i + D) % L);
+                if (m == 1) __builtin_amdgcn_sched_barrier(0);
             }
             if (s + k < s1) {
                 red.v[turn][wave][0][lane] = acc[0];
@@ -390,7 +423,7 @@ __device__ __forceinline__ void load_rows(const uint16_t* row, bool in, int u0, 
             for (int j = 0; j < FM::kSub; ++j) {
                 u32x4 v = {0, 0, 0, 0};
                 if (in && u < cnt)
-                    v = *reinterpret_cast<const u32x4*>(row + (u0 + u) * FM::kUnit + (q * 4 + g) * FM::kSub * 8 + j * 8);
+                    v = *reinterpret_cast<const u32x4*>(row + (u0 + u) * FM::kUnit + ((g * FM::kLoads + q) * FM::kSub + j) * 8);
                 b[(u * FM::kLoads + q) * FM::kSub + j] = __builtin_bit_cast(bf16x8, v);
             }
 }
