@@ -5,12 +5,17 @@
 //
 // Bound by the live experts' weights, each read once. A step is 16 weight rows
 // of two streams (gate and up; in the down projection, two neighbours) times up
-// to 16 rows of one expert: the weights go from memory into the registers as
-// operands of v_mfma_f32_16x16x32_bf16 (codes are widened to bf16, exactly), the
-// rows' values stay in registers from step to step. The eight waves of a
-// workgroup share K; their sums meet in LDS. A workgroup takes a run of
-// neighbouring steps, so that it changes its expert rarely, and holds up to 16
-// loads of 16 bytes a lane in flight across steps.
+// to 16 rows of one expert, on v_mfma_f32_16x16x32_bf16 (codes are widened to
+// bf16, exactly); the rows' values stay in registers from step to step. The eight
+// waves of a workgroup share K; each brings its own weights through a ring of
+// copies in LDS that runs across steps (12 to 14 KB in flight a wave), and their
+// sums meet in LDS. A workgroup takes a run of neighbouring steps, so that it
+// changes its expert rarely.
+//
+// The copies are what the ring is for: 64 lanes that load operands straight into
+// registers touch 64 places of 16 bytes (lanes of a row are 16 apart), each a
+// lookup of its own in the cache in front, which was busy two thirds of the time
+// that way; a copy's lanes read 64 or 128 bytes of a row in turn.
 //
 // h = silu(g) u is kept as two bf16 (value and remainder), so that it carries 16
 // bits into the down projection; its sums are kept in fp32 for each assignment
@@ -87,15 +92,16 @@ __global__ __launch_bounds__(256) void few_logits_kernel(int T, int H, int E, co
 
 // -------------------------------------------------------------- the choice --
 struct Tables {
-    uint32_t mask[256];              // tokens that chose the expert
-    int16_t base[256];               // its first row
-    int16_t id[kMaxAssign], row_of[kMaxAssign];
-    float w[kMaxAssign];
     uint8_t tok[kMaxAssign];         // token of a row
     int16_t entry_e[kMaxEntries], entry_row[kMaxEntries];
     uint8_t entry_n[kMaxEntries];
     int sums[2][kWaves];
     int entries;                     // of routed experts
+};
+struct Choosing {                    // (in the rings' place, before they start)
+    uint32_t mask[256];              // tokens that chose the expert
+    int16_t base[256];               // its first row
+    int16_t id[kMaxAssign];
 };
 
 // A score's order as an unsigned integer above 0; NaN as -infinity, -0 as 0.
@@ -121,7 +127,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 
 // Top-k of every token (a wave takes tokens wave, wave + 8, ...), then the
 // experts' rows and the entries: runs of up to 16 rows of one expert.
-__device__ void choose(const Few& f, Tables& s, bool tell)
+__device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     for (int t = wave; t < f.T; t += kWaves) {
@@ -168,20 +174,19 @@ __device__ void choose(const Few& f, Tables& s, bool tell)
         const float w = ex / moe::lanes::group_reduce<64, true>(ex);
         if (lane < f.k) {
             const int i = t * f.k + lane;
-            s.id[i] = (int16_t)my_id;
-            s.w[i] = w;
+            c.id[i] = (int16_t)my_id;
             if (tell && f.ids) f.ids[i] = my_id;
             if (tell && f.w_out) f.w_out[i] = w;
             if (tell) f.w[i] = w;
         }
         if (tell && __any(bad) && lane == 0) atomicOr(f.err, MOE_ERR_NONFINITE);
     }
-    if (tid < 256) s.mask[tid] = 0;
+    if (tid < 256) c.mask[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < f.N; i += kThreads) atomicOr(&s.mask[s.id[i]], 1u << (i / f.k));
+    for (int i = tid; i < f.N; i += kThreads) atomicOr(&c.mask[c.id[i]], 1u << (i / f.k));
     __syncthreads();
     // rows and entries before each expert (threads 0 .. 255 hold one each)
-    const int n = tid < 256 ? __popc(s.mask[tid]) : 0, tiles = (n + kTile - 1) / kTile;
+    const int n = tid < 256 ? __popc(c.mask[tid]) : 0, tiles = (n + kTile - 1) / kTile;
     int rows_to = n, tiles_to = tiles;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -199,7 +204,7 @@ __device__ void choose(const Few& f, Tables& s, bool tell)
         tiles_to += s.sums[1][w];
     }
     if (tid < 256) {
-        s.base[tid] = (int16_t)(rows_to - n);
+        c.base[tid] = (int16_t)(rows_to - n);
         for (int i = 0; i < tiles; ++i) {
             const int at = tiles_to - tiles + i;
             s.entry_e[at] = (int16_t)tid;
@@ -210,9 +215,8 @@ __device__ void choose(const Few& f, Tables& s, bool tell)
     if (tid == kThreads - 1) s.entries = tiles_to;
     __syncthreads();
     for (int i = tid; i < f.N; i += kThreads) {
-        const int t = i / f.k, e = s.id[i];
-        const int row = s.base[e] + __popc(s.mask[e] & ((1u << t) - 1u));
-        s.row_of[i] = (int16_t)row;
+        const int t = i / f.k, e = c.id[i];
+        const int row = c.base[e] + __popc(c.mask[e] & ((1u << t) - 1u));
         s.tok[row] = (uint8_t)t;
         if (tell) f.row_of[i] = row;
     }
@@ -220,37 +224,39 @@ __device__ void choose(const Few& f, Tables& s, bool tell)
 }
 
 // --------------------------------------------------------------- the forms --
-// A unit of K: kLoads loads of 16 bytes a lane, each kSub operands of 32 values
-// (8 a lane). Lane (r, g) = (lane % 16, lane / 16) holds row r, and of the unit the
-// values of bytes (g * kLoads + q) * 16 on in load q: both loads of a 128-byte unit
-// touch the whole line.
+// A unit of K: a 128-byte line of 16 weight rows, two times 16 bytes a lane, each
+// kSub operands of 32 values (8 a lane). Lane (r, g) = (lane % 16, lane / 16) takes
+// row r's chunks of 16 bytes 2 g and 2 g + 1. In LDS a row's chunks are turned so
+// that lanes of 16 rows read different banks (see lds_pipe.h). kWords: of four
+// scales, of a row's unit. (A unit of 64 bytes of 4-bit codes was slower, whether the
+// copies were kept in the caches or not: 307 and 352 us where this takes 280.)
 template <int FORM>
 struct Form;
 template <>
 struct Form<MOE_W_BF16> {
-    static constexpr int kUnit = 64, kLoads = 2, kSub = 1, kUnitBytes = 128;
+    static constexpr int kUnit = 64, kSub = 1, kWords = 0;
     __device__ static size_t bytes(size_t n) { return 2 * n; }
 };
 template <>
 struct Form<MOE_W_MX8> {
-    static constexpr int kUnit = 128, kLoads = 2, kSub = 2, kUnitBytes = 128;
+    static constexpr int kUnit = 128, kSub = 2, kWords = 1;
     __device__ static size_t bytes(size_t n) { return n; }
 };
 template <>
 struct Form<MOE_W_MX4> {
-    static constexpr int kUnit = 128, kLoads = 1, kSub = 4, kUnitBytes = 64;
+    static constexpr int kUnit = 256, kSub = 4, kWords = 2;
     __device__ static size_t bytes(size_t n) { return n / 2; }
 };
 
-// One load's operands. scales: the row's four scale bytes of the unit.
+constexpr int kUnitBytes = 128, kLoads = 2;
+
+// One load's operands. s: the scale of its block of 32 values.
 template <int FORM>
-__device__ __forceinline__ void widen(const u32x4& c, uint32_t scales, int g, bf16x8 (&o)[Form<FORM>::kSub])
+__device__ __forceinline__ void widen(const u32x4& c, float s, bf16x8 (&o)[Form<FORM>::kSub])
 {
     if constexpr (FORM == MOE_W_BF16) {
         o[0] = __builtin_bit_cast(bf16x8, c);
     } else {
-        const uint32_t byte = (scales >> (8 * g)) & 255u;
-        const float s = __uint_as_float(byte << 23);
 #pragma unroll
         for (int j = 0; j < Form<FORM>::kSub; ++j) {
             u32x4 w;
@@ -271,40 +277,40 @@ __device__ __forceinline__ void widen(const u32x4& c, uint32_t scales, int g, bf
     }
 }
 
-// Loads in flight across steps: 16, or 14 where a step's are a multiple of 7 (8 where
-// the rows' values fill the registers).
-constexpr int ring_of(int loads) { return loads % 7 == 0 ? 14 : loads == 64 ? 8 : 16; }
+// A wave's ring of weights: items are units of one stream, in the order unit, then
+// stream; kItems of them in flight, each two copies of 8 rows (1 KB). The scales of
+// a step's units come in copies of four words a row ahead of its first item, into a
+// ring of steps of their own.
+template <int FORM, int NU>
+struct Ring {
+    static constexpr int kWords = NU * Form<FORM>::kWords;
+    static constexpr int kPerStep = 2 * NU, kCopies = 2, kItems = kWords ? 6 : 7;
+    static constexpr int kScaleCopies = 2 * ((kWords + 3) / 4);             // of a step
+    static constexpr int kSteps = (kItems + kPerStep - 1) / kPerStep + 1;   // whose scales are in flight or in use
+    static constexpr int kItem = kCopies * 1024, kScales = kItems * kItem, kBytes = kScales + kSteps * kScaleCopies * 256;
+    // Copies that may still be out when items up to `landed` of a step have to be
+    // there, items up to `issued` having been started.
+    static constexpr int out(int landed, int issued)
+    {
+        return (issued - landed) * kCopies + (issued / kPerStep - landed / kPerStep) * kScaleCopies;
+    }
+};
+constexpr int kRingBytes = 14 * 1024;  // a wave's, the most of all rings
 
-// 16 bytes a lane through a buffer of `records` bytes, not kept in the caches. A
-// load past them reads nothing and gives zeros, each of its four words by itself
-// (the hardware's check of a buffer's range), so a load of nothing has records 0.
-__device__ __forceinline__ u32x4 load16(const uint8_t* base, uint32_t records, uint32_t voff, uint32_t soff)
+// Waits until at most VM of the wave's memory operations are out, and for its LDS
+// reads.
+template <int VM>
+__device__ __forceinline__ void landed()
 {
-    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)records, 0x00020000);
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 2));
+    static_assert(VM >= 0 && VM < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(VM) : "memory");
 }
 
-// N words (1, 2, 3 or 4) a lane, kept in the caches. No more than are used: a word of
-// a load in flight that nobody reads is a free register to the compiler, which then
-// waits for every load before it takes it.
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* base, uint32_t records, uint32_t voff, uint32_t soff, uint32_t* w)
+// f(0), f(1), ... with the number as a constant.
+template <typename F, int... J>
+__device__ __forceinline__ void unrolled(F f, std::integer_sequence<int, J...>)
 {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
-    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)records, 0x00020000);
-    if constexpr (N == 1) {
-        w[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0);
-    } else if constexpr (N == 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)voff, (int)soff, 0));
-        w[0] = v[0], w[1] = v[1];
-    } else if constexpr (N == 3) {
-        const u32x3 v = __builtin_bit_cast(u32x3, __builtin_amdgcn_raw_buffer_load_b96(r, (int)voff, (int)soff, 0));
-        w[0] = v[0], w[1] = v[1], w[2] = v[2];
-    } else {
-        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
-        w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
-    }
+    (f(std::integral_constant<int, J>{}), ...);
 }
 
 // The waves' sums of one step, [wave][stream][lane], doubled.
@@ -315,116 +321,156 @@ struct Reduce {
 // Steps s0 .. s1 of one entry. w, sc: the two streams' weights and scales at the
 // entry's first weight row (stream 1: up, or 16 rows on), `rows` of them, of K
 // values; step_rows weight rows from a step to the next; u0, cnt: this
-// wave's units of K. b: the rows' values of those units (NB 2: and their
-// remainders). done(step, sums of both streams) is called by one wave.
-template <int FORM, int NU, int NB, typename Done>
+// wave's units of K. load(b) fetches the rows' values of those units (NB 2: and
+// their remainders). ring: the wave's LDS. done(step, sums of both streams) is
+// called by 256 threads: thread e has weight row e / 64 % 4 * 4 + e % 4 of the
+// step's and the entry's row e / 4 % 16.
+template <int FORM, int NU, int NB, typename Load, typename Done>
 __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const uint8_t* const (&sc)[2], int K, int rows, int step_rows,
-                                          int u0, int cnt, int s0, int s1,
-                                          const bf16x8 (&b)[NB][NU * Form<FORM>::kLoads * Form<FORM>::kSub], Reduce& red,
+                                          int u0, int cnt, int s0, int s1, const char* ring, Load load, Reduce& red,
                                           int& turn, Done done)
 {
     using FM = Form<FORM>;
-    constexpr int L = 2 * NU * FM::kLoads, D0 = ring_of(L), U = D0 > L ? D0 / L : 1, D = D0 > L ? U * L : D0;
-    static_assert(L % D == 0 || D % L == 0, "ring");
-    constexpr bool kScaled = FORM != MOE_W_BF16;
+    using RG = Ring<FORM, NU>;
+    static_assert(RG::kBytes <= kRingBytes, "ring");
+    constexpr int I = RG::kPerStep, D = RG::kItems;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const uint32_t row_bytes = (uint32_t)FM::bytes(K);
-    const uint32_t voff = (uint32_t)r * row_bytes + (uint32_t)u0 * FM::kUnitBytes + 16u * FM::kLoads * g;
-    const uint32_t step_bytes = (uint32_t)step_rows * row_bytes, bytes = (uint32_t)rows * row_bytes;
-    const uint32_t srow = (uint32_t)(K / 32), svoff = (uint32_t)r * srow + 4u * u0, sstep = (uint32_t)step_rows * srow;
-    const uint8_t* const wp[2] = {uni_ptr(w[0]), uni_ptr(w[1])};
-    const uint8_t* const sp[2] = {uni_ptr(sc[0]), uni_ptr(sc[1])};
+    const uint32_t row_bytes = (uint32_t)FM::bytes(K), step_bytes = (uint32_t)step_rows * row_bytes, bytes = (uint32_t)rows * row_bytes;
+    const uint32_t srow = (uint32_t)(K / 32), sstep = (uint32_t)step_rows * srow, sbytes = (uint32_t)rows * srow;
+    const uint32_t ring_u = (uint32_t)(uintptr_t)ring;
+    // this lane's 16 bytes of a copy of 8 rows (a second copy's rows are 8 on, their
+    // chunks four places further round), and where it reads its operands
+    const int cr = lane >> 3, cc = (lane & 7) ^ moe::lds::swz(cr);
+    const uint32_t first = (uint32_t)cr * row_bytes + (uint32_t)u0 * kUnitBytes;
+    const uint32_t voff[2] = {first + 16u * cc, first + 16u * (cc ^ 4)};
+    const uint32_t svoff = (uint32_t)(lane >> 2) * srow + 4u * (u0 * FM::kWords + (lane & 3));
+    const uint32_t from[2] = {(uint32_t)(r * 128 + ((2 * g) ^ moe::lds::swz(r)) * 16),
+                              (uint32_t)(r * 128 + ((2 * g + 1) ^ moe::lds::swz(r)) * 16)};
 
-    u32x4 ring[D];
-    uint32_t next[U][2][NU];
-    // load i of the step `ahead` from s on, into its place in the ring
-    auto issue = [&](int place, int s, int ahead, int i) {
-        const int u = i / 2 / FM::kLoads, q = i / 2 % FM::kLoads;
-        ring[place] = load16(wp[i % 2], s + ahead < s1 && u < cnt ? bytes : 0u, voff,
-                             (uint32_t)(s + ahead) * step_bytes + u * FM::kUnitBytes + q * 16);
+    int to = 0, sto = 0, sat = 0;  // ring places: the next item's copies, scales' copies, scales' reads
+    auto issue = [&](int s, int j) {  // item j of step s
+        const int u = j / 2, m = j % 2;
+        if (RG::kWords && j == 0) {
+#pragma unroll
+            for (int i = 0; i < RG::kScaleCopies; ++i)
+                moe::lds::copy4(moe::lds::buffer_of(sc[i % 2], s < s1 ? sbytes : 0u), svoff, (int)((uint32_t)s * sstep + i / 2 * 16),
+                                ring_u + RG::kScales + (sto * RG::kScaleCopies + i) * 256);
+            sto = sto + 1 == RG::kSteps ? 0 : sto + 1;
+        }
+#pragma unroll
+        for (int i = 0; i < RG::kCopies; ++i)
+            moe::lds::copy16<true>(moe::lds::buffer_of(w[m], s < s1 && u < cnt ? bytes : 0u), voff[i],
+                                   (int)((uint32_t)s * step_bytes + u * kUnitBytes + i * 8 * row_bytes), ring_u + to + i * 1024);
+        to = to + RG::kItem == RG::kScales ? 0 : to + RG::kItem;
     };
-    auto scales = [&](int place, int s) {
-        if constexpr (kScaled)
+    u32x4 next[kLoads];
+    uint32_t words[2][RG::kWords ? RG::kWords : 1];
+    int at = 0;  // ring place of the next item to read
+    auto read = [&]() {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const uint32_t records = s < s1 ? (uint32_t)rows * srow : 0u, at = (uint32_t)s * sstep;
-                load_words<(NU < 4 ? NU : 4)>(sp[m], records, svoff, at, next[place][m]);
-                if constexpr (NU > 4) load_words<NU - 4>(sp[m], records, svoff, at + 16, next[place][m] + 4);
-            }
+        for (int i = 0; i < kLoads; ++i) next[i] = *reinterpret_cast<const u32x4*>(ring + at + from[i]);
+        at = at + RG::kItem == RG::kScales ? 0 : at + RG::kItem;
     };
-    // (the barriers keep the loads in this order among the products: moved behind
-    // them, each wait would be for all of them)
+    auto read_scales = [&]() {
+        if constexpr (RG::kWords > 0) {
+            const char* p = ring + RG::kScales + sat * RG::kScaleCopies * 256 + r * 16;
 #pragma unroll
-    for (int k = 0; k < U; ++k) scales(k, s0 + k);
-    __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-        issue(i, s0, i / L, i % L);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    for (int s = s0; s < s1; s += U) {
+                for (int i = 0; i < RG::kWords; ++i) words[m][i] = *reinterpret_cast<const uint32_t*>(p + (i / 4 * 2 + m) * 256 + i % 4 * 4);
+            sat = sat + 1 == RG::kSteps ? 0 : sat + 1;
+        }
+    };
+    // The scale of load i of unit u of stream m, in this lane. (Past this wave's units
+    // and past K the words are others', maybe NaN, on values of 0: half of the last
+    // unit of 256 values can be.)
+    auto scale = [&](int m, int u, int i) {
+        if constexpr (RG::kWords == 0) return 0.0f;
+        const bool in = u < cnt && (FM::kWords == 1 || (u0 + u) * FM::kUnit + g * (FM::kUnit / 4) < K);
+        const uint32_t word = FM::kWords == 1 ? words[m][u] : g < 2 ? words[m][2 * u] : words[m][2 * u + 1];
+        const uint32_t byte = word >> (FM::kWords == 1 ? 8 * g : 16 * (g & 1) + 8 * i);
+        return __uint_as_float(in ? (byte & 255u) << 23 : 0u);
+    };
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            uint32_t cur[2][NU];
-            if constexpr (kScaled) {
+    for (int j = 0; j < D; ++j) issue(s0 + j / I, j % I);
+    bf16x8 b[NB][NU * kLoads * FM::kSub];
+    load(b);
+    landed<0>();
+    read();
+    read_scales();
+    for (int s = s0; s < s1; ++s) {
+        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        float f[2][NU][FM::kWords == 2 ? 2 : 1];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < NU; ++i) cur[m][i] = i < cnt ? next[k][m][i] : 0u;  // (past cnt: other rows')
-                scales(k, s + k + U);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int m = i % 2, u = i / 2 / FM::kLoads, q = i / 2 % FM::kLoads;
+                for (int i = 0; i < (FM::kWords == 2 ? 2 : 1); ++i) f[m][u][i] = scale(m, u, i);
+        unrolled([&](auto j_tag) {
+            constexpr int j = decltype(j_tag)::value, u = j / 2, m = j % 2;
+            // the next item is there; this one is in registers and its place free
+            landed<RG::out(j + 1, j + D - 1)>();
+            u32x4 c[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) c[i] = next[i];
+            issue(s + (j + D) / I, (j + D) % I);
+            read();
+            if (j + 1 == I) read_scales();
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
                 bf16x8 a[FM::kSub];
-                widen<FORM>(ring[(k * L + i) % D], kScaled ? cur[m][u] : 0u, g, a);
+                widen<FORM>(c[i], f[m][u][FM::kWords == 2 ? i : 0], a);
 #pragma unroll
-                for (int j = 0; j < FM::kSub; ++j)
+                for (int q = 0; q < FM::kSub; ++q)
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
-                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[n][(u * FM::kLoads + q) * FM::kSub + j], acc[m], 0, 0, 0);
-                issue((k * L + i) % D, s, k + (i + D) / L, (i + D) % L);
-                if (m == 1) __builtin_amdgcn_sched_barrier(0);
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b[n][(u * kLoads + i) * FM::kSub + q], acc[m], 0, 0, 0);
             }
-            if (s + k < s1) {
-                red.v[turn][wave][0][lane] = acc[0];
-                red.v[turn][wave][1][lane] = acc[1];
-                moe::lds::wait_vm_lgkm<63>();  // the sums are in LDS; loads stay in flight
-                moe::lds::slot_barrier();
-                if (wave == (s + k) % kWaves) {
-                    f32x4 a = red.v[turn][0][0][lane], c = red.v[turn][0][1][lane];
+        }, std::make_integer_sequence<int, I>{});
+        red.v[turn][wave][0][lane] = acc[0];
+        red.v[turn][wave][1][lane] = acc[1];
+        moe::lds::wait_vm_lgkm<63>();  // the sums are in LDS; copies stay in flight
+        moe::lds::slot_barrier();
+        // one half of the waves adds them up, the other goes on, in turns: a value of
+        // each stream a thread, in the waves' order
+        if ((wave >> 2) == (s & 1)) {
+            const int e = threadIdx.x & 255;
+            float x[kWaves], y[kWaves];
 #pragma unroll
-                    for (int v = 1; v < kWaves; ++v) {
-                        a += red.v[turn][v][0][lane];
-                        c += red.v[turn][v][1][lane];
-                    }
-                    done(s + k, a, c);
-                }
-                turn ^= 1;
+            for (int v = 0; v < kWaves; ++v) {
+                x[v] = reinterpret_cast<const float*>(red.v[turn][v][0])[e];
+                y[v] = reinterpret_cast<const float*>(red.v[turn][v][1])[e];
             }
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) {
+                x[0] += x[v];
+                y[0] += y[v];
+            }
+            done(s, x[0], y[0]);
         }
+        turn ^= 1;
     }
+    landed<0>();  // copies of nothing past the last step
 }
 
-// Values of an entry's rows as operands: column n = lane % 16 is row n, `row(n)`
-// its address, of `width` bf16 values whose units u0 .. u0 + cnt are taken.
+// Values of an entry's rows as operands: lane (n, g) takes of row n, at `row`, of
+// width K, what lane (r, g) takes of a weight row in units u0 .. u0 + cnt.
 template <int FORM, int NU, int N>
-__device__ __forceinline__ void load_rows(const uint16_t* row, bool in, int u0, int cnt, bf16x8 (&b)[N])
+__device__ __forceinline__ void load_rows(const uint16_t* row, bool in, int K, int u0, int cnt, bf16x8 (&b)[N])
 {
     using FM = Form<FORM>;
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int q = 0; q < FM::kLoads; ++q)
+        for (int i = 0; i < kLoads; ++i)
 #pragma unroll
             for (int j = 0; j < FM::kSub; ++j) {
+                const int at = (u0 + u) * FM::kUnit + ((g * kLoads + i) * FM::kSub + j) * 8;
                 u32x4 v = {0, 0, 0, 0};
-                if (in && u < cnt)
-                    v = *reinterpret_cast<const u32x4*>(row + (u0 + u) * FM::kUnit + ((g * FM::kLoads + q) * FM::kSub + j) * 8);
-                b[(u * FM::kLoads + q) * FM::kSub + j] = __builtin_bit_cast(bf16x8, v);
+                if (in && u < cnt && at < K) v = *reinterpret_cast<const u32x4*>(row + at);
+                b[(u * kLoads + i) * FM::kSub + j] = __builtin_bit_cast(bf16x8, v);
             }
 }
 
@@ -442,10 +488,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
     using FM = Form<FORM>;
     __shared__ Tables tab;
     __shared__ Reduce red;
-    choose(f, tab, blockIdx.x == 0);
+    __shared__ __attribute__((aligned(1024))) char rings[kWaves * kRingBytes];
+    choose(f, tab, *reinterpret_cast<Choosing*>(rings), blockIdx.x == 0);
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
+    const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
     const int per = f.F / kTile, sper = f.SF / kTile, entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0;
-    const int units = f.H / FM::kUnit, u0 = uni(wave * units / kWaves), cnt = uni((wave + 1) * units / kWaves) - u0;
+    const int units = (f.H + FM::kUnit - 1) / FM::kUnit, u0 = uni(wave * units / kWaves), cnt = uni((wave + 1) * units / kWaves) - u0;
+    const char* ring = rings + wave * kRingBytes;
     int at, end, turn = 0;
     my_run((int64_t)entries * per + (int64_t)sentries * sper, at, end);
     while (at < end) {
@@ -460,26 +509,18 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
                                      (shared ? f.sup : f.up) + FM::bytes(first * f.H)};
         const uint8_t* const sc[2] = {(shared ? f.sgate_s : f.gate_s) + first * (f.H / 32),
                                       (shared ? f.sup_s : f.up_s) + first * (f.H / 32)};
-        bf16x8 b[1][NU * FM::kLoads * FM::kSub];
         const int tok = n < rows ? (shared ? row0 + n : (int)tab.tok[row0 + n]) : 0;
-        load_rows<FORM, NU>(f.x + (size_t)tok * f.H, n < rows, u0, cnt, b[0]);
+        auto load = [&](auto& b) { load_rows<FORM, NU>(f.x + (size_t)tok * f.H, n < rows, f.H, u0, cnt, b[0]); };
         const int width = shared ? f.SF : f.F;
-        uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + n) * width + (lane >> 4) * 4;
-        run_steps<FORM, NU, 1>(w, sc, f.H, width, kTile, u0, cnt, s0, s1, b, red, turn, [&](int s, const f32x4& g, const f32x4& u) {
-            uint32_t hi[2], lo[2];
-            float v[4], rest[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = moe::silu(g[i]) * u[i];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                hi[i] = moe::pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                rest[2 * i] = v[2 * i] - __uint_as_float(hi[i] << 16);
-                rest[2 * i + 1] = v[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
-                lo[i] = moe::pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
-            }
-            if (n < rows) {
-                *reinterpret_cast<uint2*>(h + s * kTile) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(h + f.plane + s * kTile) = make_uint2(lo[0], lo[1]);
+        uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + en) * width + ew;
+        run_steps<FORM, NU, 1>(w, sc, f.H, width, kTile, u0, cnt, s0, s1, ring, load, red, turn, [&](int s, float g, float u) {
+            // (an even thread stores its neighbour's column too)
+            const float v = moe::silu(g) * u, v1 = moe::lanes::dpp<moe::lanes::kQuadXor1>(v);
+            const uint32_t hi = moe::pack_bf16x2(v, v1);
+            const uint32_t lo = moe::pack_bf16x2(v - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
+            if (en < rows && threadIdx.x % 2 == 0) {
+                *reinterpret_cast<uint32_t*>(h + s * kTile) = hi;
+                *reinterpret_cast<uint32_t*>(h + f.plane + s * kTile) = lo;
             }
         });
         at += s1 - s0;
@@ -493,9 +534,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
     using FM = Form<FORM>;
     __shared__ Tables tab;
     __shared__ Reduce red;
-    choose(f, tab, false);
+    __shared__ __attribute__((aligned(1024))) char rings[kWaves * kRingBytes];
+    choose(f, tab, *reinterpret_cast<Choosing*>(rings), false);
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
+    const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
     const int entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0, each = f.H / (2 * kTile);
+    const char* ring = rings + wave * kRingBytes;
     int at, end, turn = 0;
     my_run((int64_t)each * (entries * f.parts + sentries * f.sparts), at, end);
     while (at < end) {
@@ -507,7 +551,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
         const int e = shared ? 0 : uni((int)tab.entry_e[entry]);
         const int row0 = shared ? entry * kTile : uni((int)tab.entry_row[entry]);
         const int rows = shared ? min(kTile, f.T - row0) : uni((int)tab.entry_n[entry]);
-        const int K = shared ? f.SF : f.F, units = K / FM::kUnit;
+        const int K = shared ? f.SF : f.F, units = (K + FM::kUnit - 1) / FM::kUnit;
         const int p0 = uni(part * units / parts), pn = uni((part + 1) * units / parts) - p0;
         const int u0 = p0 + uni(wave * pn / kWaves), cnt = p0 + uni((wave + 1) * pn / kWaves) - u0;
         const size_t first = (size_t)e * f.H;
@@ -515,16 +559,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
         const uint8_t* sbase = (shared ? f.sdown_s : f.down_s) + first * (K / 32);
         const uint8_t* const w[2] = {base, base + FM::bytes((size_t)kTile * K)};
         const uint8_t* const sc[2] = {sbase, sbase + kTile * (K / 32)};
-        bf16x8 b[2][NU * FM::kLoads * FM::kSub];
         const uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + (n < rows ? n : 0)) * K;
-        load_rows<FORM, NU>(h, n < rows, u0, cnt, b[0]);
-        load_rows<FORM, NU>(h + f.plane, n < rows, u0, cnt, b[1]);
+        auto load = [&](auto& b) {
+            load_rows<FORM, NU>(h, n < rows, K, u0, cnt, b[0]);
+            load_rows<FORM, NU>(h + f.plane, n < rows, K, u0, cnt, b[1]);
+        };
         float* y = (shared ? f.ys + (size_t)part * f.T * f.H : f.y + (size_t)part * f.N * f.H) +
-                   (size_t)(row0 + n) * f.H + (lane >> 4) * 4;
-        run_steps<FORM, NU, 2>(w, sc, K, f.H - kTile, 2 * kTile, u0, cnt, s0, s1, b, red, turn, [&](int s, const f32x4& a, const f32x4& c) {
-            if (n < rows) {
-                *reinterpret_cast<f32x4*>(y + s * 2 * kTile) = a;
-                *reinterpret_cast<f32x4*>(y + s * 2 * kTile + kTile) = c;
+                   (size_t)(row0 + en) * f.H + ew;
+        run_steps<FORM, NU, 2>(w, sc, K, f.H - kTile, 2 * kTile, u0, cnt, s0, s1, ring, load, red, turn, [&](int s, float a, float c) {
+            if (en < rows) {
+                y[s * 2 * kTile] = a;
+                y[s * 2 * kTile + kTile] = c;
             }
         });
         at += s1 - s0;
@@ -576,26 +621,53 @@ hipError_t launch_logits(const moe_shape_t& s, const MoeFew& a, float* logits, h
     return hipGetLastError();
 }
 
-// Units of K that a wave takes at most, as the kernels' NU.
+// Units of K that a wave takes at most, as the kernels' NU: 8192 values of H, 4096
+// of a part of F.
 template <int FORM>
 hipError_t launch_form(const Few& f, hipStream_t st)
 {
-    constexpr int V = FORM == MOE_W_BF16 ? 2 : 1;  // a unit of bf16 is half as long
     const int unit = Form<FORM>::kUnit, grid = cu_count();
-    auto waves = [](int units) { return (units + kWaves - 1) / kWaves; };
-    const int gu = waves(f.H / unit);
-    if (gu <= V) few_gateup_kernel<FORM, V><<<grid, kThreads, 0, st>>>(f);
-    else if (gu <= 2 * V) few_gateup_kernel<FORM, 2 * V><<<grid, kThreads, 0, st>>>(f);
-    else if (gu <= 4 * V) few_gateup_kernel<FORM, 4 * V><<<grid, kThreads, 0, st>>>(f);
-    else if (gu <= 7 * V) few_gateup_kernel<FORM, 7 * V><<<grid, kThreads, 0, st>>>(f);
-    else few_gateup_kernel<FORM, 8 * V><<<grid, kThreads, 0, st>>>(f);
-    hipError_t e = hipGetLastError();
+    auto most = [&](int K, int parts) {
+        const int units = (K + unit - 1) / unit, part = parts ? (units + parts - 1) / parts : 0;
+        return (part + kWaves - 1) / kWaves;
+    };
+    const int gu = most(f.H, 1);
+    const int dn = most(f.F, f.parts) > most(f.SF, f.sparts) ? most(f.F, f.parts) : most(f.SF, f.sparts);
+#define MOE_FEW(N) few_gateup_kernel<FORM, N><<<grid, kThreads, 0, st>>>(f)
+    if constexpr (FORM == MOE_W_BF16) {
+        if (gu <= 2) MOE_FEW(2);
+        else if (gu <= 4) MOE_FEW(4);
+        else if (gu <= 8) MOE_FEW(8);
+        else if (gu <= 14) MOE_FEW(14);
+        else MOE_FEW(16);
+    } else if constexpr (FORM == MOE_W_MX8) {
+        if (gu <= 1) MOE_FEW(1);
+        else if (gu <= 2) MOE_FEW(2);
+        else if (gu <= 4) MOE_FEW(4);
+        else if (gu <= 7) MOE_FEW(7);
+        else MOE_FEW(8);
+    } else {
+        if (gu <= 1) MOE_FEW(1);
+        else if (gu <= 2) MOE_FEW(2);
+        else MOE_FEW(4);
+    }
+#undef MOE_FEW
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    auto part = [&](int K) { return K ? waves((K / unit + moe::few_parts(K) - 1) / moe::few_parts(K)) : 0; };
-    const int dn = part(f.F) > part(f.SF) ? part(f.F) : part(f.SF);
-    if (dn <= V) few_down_kernel<FORM, V><<<grid, kThreads, 0, st>>>(f);
-    else if (dn <= 2 * V) few_down_kernel<FORM, 2 * V><<<grid, kThreads, 0, st>>>(f);
-    else few_down_kernel<FORM, 4 * V><<<grid, kThreads, 0, st>>>(f);
+#define MOE_FEW(N) few_down_kernel<FORM, N><<<grid, kThreads, 0, st>>>(f)
+    if constexpr (FORM == MOE_W_BF16) {
+        if (dn <= 2) MOE_FEW(2);
+        else if (dn <= 4) MOE_FEW(4);
+        else MOE_FEW(8);
+    } else if constexpr (FORM == MOE_W_MX8) {
+        if (dn <= 1) MOE_FEW(1);
+        else if (dn <= 2) MOE_FEW(2);
+        else MOE_FEW(4);
+    } else {
+        if (dn <= 1) MOE_FEW(1);
+        else MOE_FEW(2);
+    }
+#undef MOE_FEW
     return hipGetLastError();
 }
 

@@ -171,40 +171,6 @@ __device__ __forceinline__ float fast_silu(float z)
     return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
-// Global -> LDS copies through a buffer descriptor whose range is a register:
-// 16 bytes per lane (lane l's land at lds + 16 l) or 4 (at lds + 4 l). A lane
-// whose offset is past the range reads nothing and lands zeros: kZeroRow for
-// padding rows, range 0 for a whole copy of nothing.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t range)
-{
-    const uint64_t b = (uint64_t)(uintptr_t)base;
-    i32x4 r;
-    r[0] = uni((int32_t)(uint32_t)b);
-    r[1] = uni((int32_t)(uint32_t)(b >> 32));  // stride 0, no swizzle
-    r[2] = (int32_t)range;
-    r[3] = 0x00020000;                         // data format 32
-    return r;
-}
-// STREAM: not kept in the caches.
-template <bool STREAM = false>
-__device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
-{
-    if (STREAM)
-        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-                     :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                     :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4(const i32x4& rsrc, uint32_t voff, int soff, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"((int)lds) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
 __device__ __forceinline__ i32x8 frag(const char* p0, const char* p1)
 {
     const u32x4 a = *reinterpret_cast<const u32x4*>(p0), b = *reinterpret_cast<const u32x4*>(p1);
