@@ -44,6 +44,7 @@ constexpr int kMaxEntries = 256 + kMaxAssign / (kTile + 1) + 1; // experts, and 
 // rows N .. N + T - 1 the shared expert's.
 struct Few {
     int T, H, E, k, F, SF, N;
+    int planes;                      // of the router's scores
     int parts, sparts;               // of K in the down projection
     const uint16_t* x;
     const float *logits, *bias;
@@ -58,36 +59,47 @@ struct Few {
 };
 
 // --------------------------------------------------------- router's scores --
-// One workgroup an expert: its row against every token's, fp32 sums in an order
-// fixed by H.
-template <int TT>
-__global__ __launch_bounds__(256) void few_logits_kernel(int T, int H, int E, const uint16_t* __restrict__ x,
-                                                         const uint16_t* __restrict__ wr, float* __restrict__ logits)
+// 16 experts against every token over a part of H: each of eight waves takes up to
+// kLogitSteps x 32 values of K, their sums meet in LDS, and the parts' are added by
+// the choice, in order. (One workgroup an expert on the vector unit took 20 us for
+// 16 tokens of 7168; this takes 5.)
+constexpr int kLogitSteps = 4;
+
+template <int NT>
+__global__ __launch_bounds__(kThreads) void few_logits_kernel(int T, int H, int E, const uint16_t* __restrict__ x,
+                                                              const uint16_t* __restrict__ wr, float* __restrict__ logits)
 {
-    __shared__ float red[4][TT];
-    const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float acc[TT];
+    __shared__ f32x4 red[kWaves][NT][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int e = min((int)blockIdx.x * kTile + r, E - 1);
+    const int k0 = ((int)blockIdx.y * kWaves + wave) * (kLogitSteps * 32) + g * 8;
+    const u32x4 none = {0, 0, 0, 0};
+    u32x4 a[kLogitSteps], b[NT][kLogitSteps];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
-    for (int c = tid * 8; c < H; c += 256 * 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(wr + (size_t)e * H + c);
+    for (int i = 0; i < kLogitSteps; ++i) {
+        const int k = k0 + i * 32;
+        a[i] = k < H ? *reinterpret_cast<const u32x4*>(wr + (size_t)e * H + k) : none;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(x + (size_t)(t < T ? t : 0) * H + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[t] = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(v[i] << 16), acc[t]);
-                acc[t] = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), acc[t]);
-            }
-        }
+        for (int n = 0; n < NT; ++n)
+            b[n][i] = k < H && n * kTile + r < T ? *reinterpret_cast<const u32x4*>(x + (size_t)(n * kTile + r) * H + k) : none;
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        const float s = moe::lanes::group_reduce<64, true>(acc[t]);
-        if (lane == 0) red[wave][t] = s;
+    for (int n = 0; n < NT; ++n) {
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kLogitSteps; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b[n][i]), acc, 0, 0, 0);
+        red[wave][n][lane] = acc;
     }
     __syncthreads();
-    if (tid < T) logits[(size_t)tid * E + e] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+    // value i of lane l: expert l / 16 * 4 + i, token l % 16
+    for (int v = tid; v < NT * 256; v += kThreads) {
+        const int n = v / 256, i = v % 256, t = n * kTile + i / 4 % 16, ex = blockIdx.x * kTile + i / 64 * 4 + i % 4;
+        float sum = reinterpret_cast<const float*>(red[0][n])[i];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const float*>(red[w][n])[i];
+        if (t < T && ex < E) logits[((size_t)blockIdx.y * T + t) * E + ex] = sum;
+    }
 }
 
 // -------------------------------------------------------------- the choice --
@@ -140,7 +152,14 @@ __device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
             lg[p] = 0.0f;
             key[p] = 0;
             if (e < f.E) {
-                const float l = f.logits[(size_t)t * f.E + e], b = f.bias ? f.bias[e] : 0.0f;
+                const float* at = f.logits + (size_t)t * f.E + e;
+                float v[moe::kFewLogitParts];
+#pragma unroll
+                for (int q = 0; q < moe::kFewLogitParts; ++q) v[q] = q < f.planes ? at[(size_t)q * f.T * f.E] : 0.0f;
+                float l = v[0];
+#pragma unroll
+                for (int q = 1; q < moe::kFewLogitParts; ++q) l += v[q];
+                const float b = f.bias ? f.bias[e] : 0.0f;
                 bad |= !isfinite(l) || !isfinite(b);
                 lg[p] = l;
                 key[p] = order_of(l + b);
@@ -611,13 +630,11 @@ int cu_count()
 
 hipError_t launch_logits(const moe_shape_t& s, const MoeFew& a, float* logits, hipStream_t st)
 {
+    static_assert(moe::kFewLogitK == kWaves * kLogitSteps * 32, "a workgroup's part of H");
     const uint16_t *x = static_cast<const uint16_t*>(a.x), *w = static_cast<const uint16_t*>(a.w_router);
-    if (s.T <= 1) few_logits_kernel<1><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
-    else if (s.T <= 2) few_logits_kernel<2><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
-    else if (s.T <= 4) few_logits_kernel<4><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
-    else if (s.T <= 8) few_logits_kernel<8><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
-    else if (s.T <= 16) few_logits_kernel<16><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
-    else few_logits_kernel<32><<<s.E, 256, 0, st>>>(s.T, s.H, s.E, x, w, logits);
+    const dim3 grid((s.E + kTile - 1) / kTile, moe::few_logit_parts(s.H));
+    if (s.T <= kTile) few_logits_kernel<1><<<grid, kThreads, 0, st>>>(s.T, s.H, s.E, x, w, logits);
+    else few_logits_kernel<2><<<grid, kThreads, 0, st>>>(s.T, s.H, s.E, x, w, logits);
     return hipGetLastError();
 }
 
@@ -680,6 +697,7 @@ hipError_t moe_launch_few(const moe_shape_t& s, const MoeFew& a, char* ws, hipSt
     auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
     Few f;
     f.T = s.T, f.H = s.H, f.E = s.E, f.k = s.k, f.F = s.F, f.SF = a.shared_F, f.N = s.T * s.k;
+    f.planes = moe::few_logit_parts(s.H);
     f.parts = moe::few_parts(s.F), f.sparts = moe::few_parts(a.shared_F);
     f.x = static_cast<const uint16_t*>(a.x);
     float* logits = reinterpret_cast<float*>(ws + L.logits);

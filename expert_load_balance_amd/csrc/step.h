@@ -123,10 +123,14 @@ namespace moe {
 constexpr int kFewMaxH = 8192;   // a wave's part of a row of x stays in registers
 constexpr int kFewPart = 4096;   // values of K of a part of the down projection (h in registers, two bf16 each)
 
+constexpr int kFewLogitK = 1024; // values of H of a part of the router's scores
+constexpr int kFewLogitParts = kFewMaxH / kFewLogitK;
+
+inline int few_logit_parts(int H) { return (H + kFewLogitK - 1) / kFewLogitK; }
 inline int few_unit(int form) { return form == MOE_W_BF16 ? 64 : 128; }
 inline int few_parts(int F) { return (F + kFewPart - 1) / kFewPart; }
 
-// logits [T][E], the router's w [N] and each assignment's row [N], h in two bf16
+// logits [parts][T][E], the router's w [N] and each assignment's row [N], h in two bf16
 // planes [N][F] + [T][shared_F], y fp32 [parts][N][H] + [shared parts][T][H]
 struct FewWsLayout {
     size_t logits, w, row_of, h, y, total;
@@ -138,7 +142,7 @@ inline FewWsLayout few_ws_layout(const moe_shape_t& s, int shared_F)
     const size_t N = (size_t)s.T * s.k, n1 = N > 0 ? N : 1;
     FewWsLayout w;
     size_t o = 0;
-    w.logits = o; o = align256(o + ((size_t)s.T * s.E + 1) * 4);
+    w.logits = o; o = align256(o + ((size_t)few_logit_parts(s.H) * s.T * s.E + 1) * 4);
     w.w = o;      o = align256(o + n1 * 4);
     w.row_of = o; o = align256(o + n1 * 4);
     w.h_shared = N * s.F;
