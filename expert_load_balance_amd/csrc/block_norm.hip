@@ -9,6 +9,7 @@
 // Bound by memory: each input is read once and each output written once. One
 // workgroup takes one row and keeps it in registers over both norms' sums, as
 // CH 16-byte vectors of x and of the residual per thread.
+#include "lanes.h"
 #include "rows.h"
 #include "step.h"
 
@@ -205,12 +206,17 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_wide_kernel(const Fwd 
 }
 
 // ---------------------------------------------------------------- backward --
-//   d = ds + rstd_pre (g - shat mean(g shat)), g = dy w_pre, shat = s rstd_pre;
+//   d = ds + rstd_pre (g - shat m), g = dy w_pre, shat = s rstd_pre, m = mean(g shat);
 //   dresidual = alpha d, dn = gate d,
 //   dx = rstd_post (e - xhat mean(e xhat)), e = dn w_post, xhat = x rstd_post.
-// A workgroup takes parts (runs of rows under one row of gates) b, b + G, ...
+// The second mean needs d, and with it the first one; taken apart it does not:
+//   sum(e xhat) = sum(a (ds + rstd_pre g)) - m sum(a rstd_pre shat), a = gate w_post xhat,
+// so that a row's three sums meet at one barrier.
+//
+// A workgroup takes parts (every n-th row under one row of gates) b, b + G, ...
 // and keeps the fp32 sums of dw_pre and dw_post of its columns over all of its
-// rows, and those of dgate over a part, so that the sums' order is fixed.
+// rows, and those of dgate over a part, so that the sums' order is fixed. The next
+// row is loaded while one is summed.
 struct Bwd {
     int H, vecs;
     int64_t T;
@@ -233,138 +239,159 @@ __device__ __forceinline__ void store_sums(float* to, const float* v)
         *reinterpret_cast<float4*>(to + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
 }
 
+// Three sums over the workgroup, in a fixed order. red: LDS that the row before
+// does not use.
+__device__ __forceinline__ void sum3(float (&v)[3], float (*red)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = moe::lanes::group_reduce<64, true>(v[i]);
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    if (waves == 1) return;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) red[i][wave] = v[i];
+    __syncthreads();
+    const int w = threadIdx.x & 15;  // (every 16 lanes add the waves' up: one read, four steps)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = red[i][w];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = moe::lanes::group_reduce<16, true>(w < waves ? v[i] : 0.0f);
+}
+
+// A part's rows: r0, r0 + per_group, ... below r1.
+struct Rows {
+    int64_t r0, r1;
+};
+__device__ __forceinline__ Rows rows_of(const Bwd& a, int64_t part)
+{
+    const int64_t group = part / a.p.per_group, r1 = (group + 1) * a.p.group_rows;
+    return Rows{group * a.p.group_rows + part % a.p.per_group, r1 < a.T ? r1 : a.T};
+}
+
+// dw_post and dgate are one sum over a part's rows, A = sum(token's gate * d xhat),
+// times a column's gate and times its weight.
 template <bool BF16, int CH, int TH, bool STREAM>
 __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(const Bwd a)
 {
     using V = Vec<BF16>;
     constexpr int N = V::kN;
-    __shared__ float red[2][2][16];
+    __shared__ float red[2][3][16];
     const float inv_h = 1.0f / (float)a.H;
     const uint4 none = make_uint4(0, 0, 0, 0);
-    float acc_post[CH][N], acc_pre[CH][N], acc_gate[CH][N];
-    uint4 w1[CH], w2[CH], gv[CH];
+    float acc[CH][N], acc_post[CH][N], acc_pre[CH][N];
+    float w2[CH][N], gw[CH][N];  // w_pre, gate * w_post
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = i * blockDim.x + threadIdx.x;
-        w1[i] = c < a.vecs && a.w_post ? a.w_post[c] : none;
-        w2[i] = c < a.vecs && a.w_pre ? a.w_pre[c] : none;
+        V::load(c < a.vecs && a.w_pre ? a.w_pre[c] : none, w2[i]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc_post[i][k] = acc_pre[i][k] = acc_gate[i][k] = 0.0f;
+        for (int k = 0; k < N; ++k) acc[i][k] = acc_post[i][k] = acc_pre[i][k] = 0.0f;
     }
-    int turn = 0;
-    for (int64_t part = blockIdx.x; part < a.p.parts; part += gridDim.x) {
-        const int64_t group = part / a.p.per_group, r0 = group * a.p.group_rows + part % a.p.per_group * a.p.part_rows;
-        int64_t r1 = (group + 1) * a.p.group_rows;
-        r1 = r1 < r0 + a.p.part_rows ? r1 : r0 + a.p.part_rows;
-        r1 = r1 < a.T ? r1 : a.T;
-        const uint4* gr = gate_row(a.gate, a.gate_rows, r0, a.vecs);
+    uint4 nx[CH], ns[CH], nd[CH], ne[CH];  // the next row
+    float n1 = 1.0f, n2 = 0.0f, ng = 1.0f;
+    auto load = [&](int64_t row) {
+        if (a.w_post) n1 = a.rstd_post[row];
+        if (a.dy) n2 = a.rstd_pre[row];
+        ng = token_gate<BF16>(a.gate, a.gate_rows, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
-            gv[i] = gr && c < a.vecs ? gr[c] : none;
+            const int64_t at = row * a.vecs + c;
+            nx[i] = ns[i] = nd[i] = ne[i] = none;
+            if (c < a.vecs) {
+                nx[i] = moe::load16<STREAM>(a.x + at);
+                if (a.dy) {
+                    ns[i] = moe::load16<STREAM>(a.s + at);
+                    nd[i] = moe::load16<STREAM>(a.dy + at);
+                }
+                if (a.ds) ne[i] = moe::load16<STREAM>(a.ds + at);
+            }
         }
-        for (int64_t row = r0; row < r1; ++row, turn ^= 1) {
+    };
+    // this thread's columns of w_post and of the part's gates (1 where there is none)
+    auto column = [&](const uint4* from, int i, float* v) {
+        const int c = i * blockDim.x + threadIdx.x;
+        if (from) V::load(c < a.vecs ? from[c] : none, v);
+        else
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = 1.0f;
+    };
+    int turn = 0;
+    for (int64_t part = blockIdx.x; part < a.p.parts; part += gridDim.x) {
+        const Rows rows = rows_of(a, part);
+        const uint4* gr = gate_row(a.gate, a.gate_rows, rows.r0, a.vecs);
+        if (rows.r0 < rows.r1) load(rows.r0);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float w[N], g[N];
+            column(a.w_post, i, w);
+            column(gr, i, g);
+#pragma unroll
+            for (int k = 0; k < N; ++k) gw[i][k] = g[k] * w[k];
+        }
+        for (int64_t row = rows.r0; row < rows.r1; row += a.p.per_group, turn ^= 1) {
             const int64_t base = row * a.vecs;
-            const float tg = token_gate<BF16>(a.gate, a.gate_rows, row);
-            const float rs1 = a.w_post ? a.rstd_post[row] : 1.0f, rs2 = a.dy ? a.rstd_pre[row] : 0.0f;
-            uint4 ux[CH], us[CH], ud[CH], ue[CH];
+            const float tg = ng, rs1 = n1, rs2 = n2;
+            // xhat, shat, and d but for the first mean
+            float xh[CH][N], sh[CH][N], d[CH][N], sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int c = i * blockDim.x + threadIdx.x;
-                ux[i] = us[i] = ud[i] = ue[i] = none;
-                if (c < a.vecs) {
-                    ux[i] = moe::load16<STREAM>(a.x + base + c);
-                    if (a.dy) {
-                        us[i] = moe::load16<STREAM>(a.s + base + c);
-                        ud[i] = moe::load16<STREAM>(a.dy + base + c);
-                    }
-                    if (a.ds) ue[i] = moe::load16<STREAM>(a.ds + base + c);
-                }
-            }
-            float d[CH][N], dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) V::load(ue[i], d[i]);
-            if (a.dy) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    float sv[N], g[N], w[N];
-                    V::load(us[i], sv);
-                    V::load(ud[i], g);
-                    V::load(w2[i], w);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const float sh = sv[k] * rs2;
-                        acc_pre[i][k] = fmaf(g[k], sh, acc_pre[i][k]);
-                        dot = fmaf(g[k] * w[k], sh, dot);
-                    }
-                }
-                const float mean = wg_sum(dot, red[turn][0]) * inv_h;
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    float sv[N], g[N], w[N];
-                    V::load(us[i], sv);
-                    V::load(ud[i], g);
-                    V::load(w2[i], w);
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        d[i][k] = fmaf(rs2, fmaf(-(sv[k] * rs2), mean, g[k] * w[k]), d[i][k]);
-                }
-            }
-            if (a.dresidual)
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int c = i * blockDim.x + threadIdx.x;
-                    float v[N];
-#pragma unroll
-                    for (int k = 0; k < N; ++k) v[k] = a.alpha * d[i][k];
-                    if (c < a.vecs) moe::store16<STREAM>(a.dresidual + base + c, V::store(v));
-                }
-            // xhat (x without a norm behind) and what reaches it
-            dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float x[N], w[N], g[N];
-                V::load(ux[i], x);
-                V::load(w1[i], w);
-                V::load(gv[i], g);
+                float dy[N];
+                V::load(nx[i], xh[i]);
+                V::load(ns[i], sh[i]);
+                V::load(nd[i], dy);
+                V::load(ne[i], d[i]);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float xh = x[k] * rs1, n = a.w_post ? xh * w[k] : xh;
-                    acc_gate[i][k] = fmaf(d[i][k], n, acc_gate[i][k]);
-                    const float dn = gr ? d[i][k] * g[k] : d[i][k];  // (a token's gate follows)
-                    acc_post[i][k] = fmaf(dn * tg, xh, acc_post[i][k]);
-                    dot = fmaf(gr ? dn * w[k] : d[i][k], gr ? xh : n, dot);
-                    d[i][k] = dn * tg;
+                    xh[i][k] *= rs1;
+                    sh[i][k] *= rs2;
+                    const float g = dy[k] * w2[i][k], p = xh[i][k] * gw[i][k];
+                    acc_pre[i][k] = fmaf(dy[k], sh[i][k], acc_pre[i][k]);
+                    d[i][k] = fmaf(rs2, g, d[i][k]);
+                    sum[0] = fmaf(g, sh[i][k], sum[0]);
+                    sum[1] = fmaf(p, d[i][k], sum[1]);
+                    sum[2] = fmaf(p, sh[i][k], sum[2]);
                 }
             }
-            float mean = 0.0f;
-            if (a.w_post || a.token_dgate) {
-                // without a row of gates: sum d n, a token's dgate; it times the gate is
-                // the sum that dx needs
-                dot = wg_sum(dot, red[turn][1]);
-                if (a.token_dgate && threadIdx.x == 0) a.token_dgate[row] = dot;
-                mean = a.w_post ? dot * tg * inv_h : 0.0f;
-            }
+            // (dx or dresidual may be dy or ds: this row is in registers before it is
+            // stored, and the next one is another)
+            if (row + a.p.per_group < rows.r1) load(row + a.p.per_group);
+            sum3(sum, red[turn]);
+            const float m = sum[0] * inv_h * rs2, dot = fmaf(-m, sum[2], sum[1]);
+            // without a row of gates dot is sum(d n): a token's dgate
+            if (a.token_dgate && threadIdx.x == 0) a.token_dgate[row] = dot;
+            const float r = tg * rs1, mean = a.w_post ? dot * inv_h : 0.0f;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int c = i * blockDim.x + threadIdx.x;
-                float x[N], w[N];
-                V::load(ux[i], x);
-                V::load(w1[i], w);
-                if (a.w_post)
+                float v[N];
 #pragma unroll
-                    for (int k = 0; k < N; ++k) d[i][k] = rs1 * fmaf(-(x[k] * rs1), mean, d[i][k] * w[k]);
-                if (c < a.vecs) moe::store16<STREAM>(a.dx + base + c, V::store(d[i]));
+                for (int k = 0; k < N; ++k) {
+                    const float dk = fmaf(-m, sh[i][k], d[i][k]);
+                    acc[i][k] = fmaf(tg * dk, xh[i][k], acc[i][k]);
+                    v[k] = r * fmaf(-mean, xh[i][k], dk * gw[i][k]);
+                    d[i][k] = a.alpha * dk;
+                }
+                if (c < a.vecs) {
+                    if (a.dresidual) moe::store16<STREAM>(a.dresidual + base + c, V::store(d[i]));
+                    moe::store16<STREAM>(a.dx + base + c, V::store(v));
+                }
             }
         }
-        if (a.part_gate)
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = i * blockDim.x + threadIdx.x;
-                if (c < a.vecs) store_sums<N>(a.part_gate + part * a.H + (int64_t)c * N, acc_gate[i]);
+        for (int i = 0; i < CH; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            float w[N], g[N];
+            column(a.w_post, i, w);
+            column(gr, i, g);
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc_gate[i][k] = 0.0f;
+            for (int k = 0; k < N; ++k) {
+                acc_post[i][k] = fmaf(g[k], acc[i][k], acc_post[i][k]);
+                w[k] *= acc[i][k];
+                acc[i][k] = 0.0f;
             }
+            if (a.part_gate && c < a.vecs) store_sums<N>(a.part_gate + part * a.H + (int64_t)c * N, w);
+        }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -375,14 +402,14 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(const Bwd a)
     }
 }
 
-// Rows too wide for the registers: the sums are kept in the workspace, d is
-// computed again where it is needed.
+// Rows too wide for the registers: the sums are kept in the workspace, two passes
+// over the row.
 template <bool BF16>
 __global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_wide_kernel(const Bwd a)
 {
     using V = Vec<BF16>;
     constexpr int N = V::kN;
-    __shared__ float red[2][2][16];
+    __shared__ float red[2][3][16];
     const float inv_h = 1.0f / (float)a.H;
     const uint4 none = make_uint4(0, 0, 0, 0);
     const int64_t mine = (int64_t)blockIdx.x * a.H;
@@ -392,90 +419,69 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_wide_kernel(const 
 #pragma unroll
             for (int k = 0; k < N; ++k) sums[(int64_t)c * N + k] = 0.0f;
     };
+    auto add = [&](float* sums, int c, const float* v) {
+        if (!sums) return;
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            float4* p = reinterpret_cast<float4*>(sums + (int64_t)c * N + k);
+            const float4 o = *p;
+            *p = make_float4(o.x + v[k], o.y + v[k + 1], o.z + v[k + 2], o.w + v[k + 3]);
+        }
+    };
     clear(a.part_post ? a.part_post + mine : nullptr);
     clear(a.part_pre ? a.part_pre + mine : nullptr);
     int turn = 0;
     for (int64_t part = blockIdx.x; part < a.p.parts; part += gridDim.x) {
-        const int64_t group = part / a.p.per_group, r0 = group * a.p.group_rows + part % a.p.per_group * a.p.part_rows;
-        int64_t r1 = (group + 1) * a.p.group_rows;
-        r1 = r1 < r0 + a.p.part_rows ? r1 : r0 + a.p.part_rows;
-        r1 = r1 < a.T ? r1 : a.T;
-        const uint4* gr = gate_row(a.gate, a.gate_rows, r0, a.vecs);
+        const Rows rows = rows_of(a, part);
+        const uint4* gr = gate_row(a.gate, a.gate_rows, rows.r0, a.vecs);
         clear(a.part_gate ? a.part_gate + part * a.H : nullptr);
-        for (int64_t row = r0; row < r1; ++row, turn ^= 1) {
+        for (int64_t row = rows.r0; row < rows.r1; row += a.p.per_group, turn ^= 1) {
             const int64_t base = row * a.vecs;
             const float tg = token_gate<BF16>(a.gate, a.gate_rows, row);
             const float rs1 = a.w_post ? a.rstd_post[row] : 1.0f, rs2 = a.dy ? a.rstd_pre[row] : 0.0f;
-            float dot = 0.0f, mean1 = 0.0f;
-            if (a.dy) {
-                for (int c = threadIdx.x; c < a.vecs; c += blockDim.x) {
-                    float sv[N], g[N], w[N];
-                    V::load(a.s[base + c], sv);
-                    V::load(a.dy[base + c], g);
-                    V::load(a.w_pre[c], w);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const float sh = sv[k] * rs2;
-                        if (a.part_pre) {
-                            float* p = a.part_pre + mine + (int64_t)c * N + k;
-                            *p = fmaf(g[k], sh, *p);
-                        }
-                        dot = fmaf(g[k] * w[k], sh, dot);
-                    }
-                }
-                mean1 = wg_sum(dot, red[turn][0]) * inv_h;
-            }
-            auto d_at = [&](int c, float* d) {
-                V::load(a.ds ? a.ds[base + c] : none, d);
-                if (!a.dy) return;
-                float sv[N], g[N], w[N];
-                V::load(a.s[base + c], sv);
-                V::load(a.dy[base + c], g);
-                V::load(a.w_pre[c], w);
-#pragma unroll
-                for (int k = 0; k < N; ++k) d[k] = fmaf(rs2, fmaf(-(sv[k] * rs2), mean1, g[k] * w[k]), d[k]);
-            };
-            dot = 0.0f;
-            for (int c = threadIdx.x; c < a.vecs; c += blockDim.x) {
-                float d[N], x[N], w[N], g[N];
-                d_at(c, d);
+            float x[N], sv[N], dy[N], d[N], w[N], v[N], g[N], sum[3] = {0.0f, 0.0f, 0.0f};
+            auto load = [&](int c) {
                 V::load(a.x[base + c], x);
+                V::load(a.dy ? a.s[base + c] : none, sv);
+                V::load(a.dy ? a.dy[base + c] : none, dy);
+                V::load(a.ds ? a.ds[base + c] : none, d);
                 V::load(a.w_post ? a.w_post[c] : none, w);
+                V::load(a.w_pre ? a.w_pre[c] : none, v);
                 V::load(gr ? gr[c] : none, g);
+            };
+            for (int c = threadIdx.x; c < a.vecs; c += blockDim.x) {
+                load(c);
+                float pre[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float xh = x[k] * rs1, n = a.w_post ? xh * w[k] : xh;
-                    const float dn = gr ? d[k] * g[k] : d[k];
-                    if (a.part_gate) {
-                        float* p = a.part_gate + part * a.H + (int64_t)c * N + k;
-                        *p = fmaf(d[k], n, *p);
-                    }
-                    if (a.part_post) {
-                        float* p = a.part_post + mine + (int64_t)c * N + k;
-                        *p = fmaf(dn * tg, xh, *p);
-                    }
-                    dot = fmaf(gr ? dn * w[k] : d[k], gr ? xh : n, dot);
+                    const float xh = x[k] * rs1, sh = sv[k] * rs2, gd = dy[k] * v[k];
+                    const float n = a.w_post ? xh * w[k] : xh, p = gr ? n * g[k] : n;
+                    pre[k] = dy[k] * sh;
+                    sum[0] = fmaf(gd, sh, sum[0]);
+                    sum[1] = fmaf(p, fmaf(rs2, gd, d[k]), sum[1]);
+                    sum[2] = fmaf(p, rs2 * sh, sum[2]);
                 }
+                add(a.part_pre ? a.part_pre + mine : nullptr, c, pre);
             }
-            float mean2 = 0.0f;
-            if (a.w_post || a.token_dgate) {
-                dot = wg_sum(dot, red[turn][1]);
-                if (a.token_dgate && threadIdx.x == 0) a.token_dgate[row] = dot;
-                mean2 = a.w_post ? dot * tg * inv_h : 0.0f;
-            }
+            sum3(sum, red[turn]);
+            const float m = sum[0] * inv_h, dot = fmaf(-m, sum[2], sum[1]), mean = dot * tg * inv_h;
+            if (a.token_dgate && threadIdx.x == 0) a.token_dgate[row] = dot;
             // (dx or dresidual may be dy or ds: a vector is stored after its last reading)
             for (int c = threadIdx.x; c < a.vecs; c += blockDim.x) {
-                float d[N], x[N], w[N], g[N], v[N];
-                d_at(c, d);
-                V::load(a.x[base + c], x);
-                V::load(a.w_post ? a.w_post[c] : none, w);
-                V::load(gr ? gr[c] : none, g);
+                load(c);
+                float gate[N], post[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float dn = (gr ? d[k] * g[k] : d[k]) * tg;
-                    v[k] = a.w_post ? rs1 * fmaf(-(x[k] * rs1), mean2, dn * w[k]) : dn;
+                    const float xh = x[k] * rs1;
+                    d[k] = fmaf(rs2, fmaf(-(sv[k] * rs2), m, dy[k] * v[k]), d[k]);
+                    gate[k] = d[k] * (a.w_post ? xh * w[k] : xh);
+                    const float dn = d[k] * (gr ? g[k] : tg);
+                    post[k] = dn * xh;
+                    v[k] = a.w_post ? rs1 * fmaf(-xh, mean, dn * w[k]) : dn;
                     d[k] *= a.alpha;
                 }
+                add(a.part_gate ? a.part_gate + part * a.H : nullptr, c, gate);
+                add(a.part_post ? a.part_post + mine : nullptr, c, post);
                 if (a.dresidual) a.dresidual[base + c] = V::store(d);
                 a.dx[base + c] = V::store(v);
             }
@@ -558,11 +564,10 @@ hipError_t launch_fwd(const Fwd& a, int rows, hipStream_t st)
 template <bool BF16, bool STREAM>
 hipError_t launch_bwd(const Bwd& a, hipStream_t st)
 {
-    int t = 64;
-    while (t < 512 && a.vecs > 2 * t) t *= 2;
-    const int ch = (a.vecs + t - 1) / t, G = a.p.grid;
-    if (ch == 1) block_norm_bwd_kernel<BF16, 1, 512, STREAM><<<G, t, 0, st>>>(a);
-    else if (ch == 2) block_norm_bwd_kernel<BF16, 2, 512, STREAM><<<G, t, 0, st>>>(a);
+    const int G = a.p.grid, t = (a.vecs + 63) / 64 * 64;
+    if (t <= 512) block_norm_bwd_kernel<BF16, 1, 512, STREAM><<<G, t, 0, st>>>(a);
+    else if (t <= 1024) block_norm_bwd_kernel<BF16, 1, 1024, STREAM><<<G, t, 0, st>>>(a);
+    else if (t <= 2048) block_norm_bwd_kernel<BF16, 2, 1024, STREAM><<<G, (a.vecs + 127) / 128 * 64, 0, st>>>(a);
     else block_norm_bwd_wide_kernel<BF16><<<G, kMaxThreads, 0, st>>>(a);
     return hipGetLastError();
 }
@@ -597,7 +602,7 @@ hipError_t moe_launch_block_norm_backward(const moe_shape_t& s, const MoeBlockNo
 {
     const bool bf = s.dtype == MOE_BF16, rows_gate = m.gate && m.gate_rows > 0 && m.dgate;
     const int32_t gate_rows = m.gate ? m.gate_rows : 0;
-    const moe::BlockNormParts p = moe::block_norm_parts(s.T, gate_rows);
+    const moe::BlockNormParts p = moe::block_norm_parts(s, gate_rows);
     if (s.T == 0) {  // sums over no rows
         if (!m.dw_post && !m.dw_pre) return hipSuccess;
         block_norm_zero_kernel<<<(s.H + 255) / 256 < 1024 ? (s.H + 255) / 256 : 1024, 256, 0, st>>>(m.dw_post, m.dw_pre, s.H);
@@ -615,7 +620,7 @@ hipError_t moe_launch_block_norm_backward(const moe_shape_t& s, const MoeBlockNo
                       : (stream ? launch_bwd<false, true> : launch_bwd<false, false>);
     hipError_t e = launch(a, st);
     if (e != hipSuccess) return e;
-    // (groups of several parts are fewer than kNormBwdGroups)
+    // (groups of several parts are fewer than the workgroups, 1024 at most)
     const int groups = rows_gate && p.per_group > 1 ? (int)p.groups : 0;
     if (!m.dw_post && !m.dw_pre && !groups) return hipSuccess;
     const Sums q{s.H, p.grid, p.per_group, a.part_post, a.part_pre, a.part_gate, m.dw_post, m.dw_pre, m.dgate};

@@ -2,7 +2,8 @@
 //
 // Bound by memory. A thread takes eight values: 16 bytes of bf16 (or 32 of
 // fp32) against 4 bytes of codes, so that a wave reads and writes whole lines;
-// four neighbouring lanes hold a block.
+// four neighbouring lanes hold a block. It has four such eights in flight.
+#include "lanes.h"
 #include "rows.h"
 #include "step.h"
 
@@ -10,68 +11,97 @@ namespace {
 
 using moe::rows::Vec;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kEach = 4;  // eights of a thread at a time
 constexpr int kMaxGrid = 16384;
 
+// An eight of values in 16-byte vectors.
 template <bool BF16>
-__device__ __forceinline__ void load8(const uint4* x, int64_t i, float* f)
-{
-    if (BF16) {
-        Vec<true>::load(x[i], f);
-    } else {
-        Vec<false>::load(x[2 * i], f);
-        Vec<false>::load(x[2 * i + 1], f + 4);
+struct Eight {
+    uint4 v[BF16 ? 1 : 2];
+    template <bool STREAM>
+    __device__ void load(const uint4* x, int64_t i)
+    {
+#pragma unroll
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k) v[k] = moe::load16<STREAM>(x + (BF16 ? 1 : 2) * i + k);
     }
-}
-template <bool BF16>
-__device__ __forceinline__ void store8(uint4* x, int64_t i, const float* f)
-{
-    if (BF16) {
-        x[i] = Vec<true>::store(f);
-    } else {
-        x[2 * i] = Vec<false>::store(f);
-        x[2 * i + 1] = Vec<false>::store(f + 4);
+    __device__ void values(float* f) const
+    {
+#pragma unroll
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k) Vec<BF16>::load(v[k], f + 4 * k);
     }
-}
+    template <bool STREAM>
+    __device__ static void store(uint4* x, int64_t i, const float* f)
+    {
+#pragma unroll
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k)
+            moe::store16<STREAM>(x + (BF16 ? 1 : 2) * i + k, Vec<BF16>::store(f + 4 * k));
+    }
+};
 
-// n: eights of values, a multiple of four
-template <bool BF16>
+// n: eights of values, a multiple of four, so that the lanes of a block pass the end
+// together and the shuffles see all of it
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(int64_t n, const uint4* __restrict__ x,
                                                                 uint32_t* __restrict__ q,
                                                                 uint8_t* __restrict__ scales)
 {
-    // (a block's lanes pass the end together, so the shuffles see all of it)
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        float f[8];
-        load8<BF16>(x, i, f);
-        uint32_t top = 0;
+    for (int64_t at = (int64_t)blockIdx.x * (kThreads * kEach); at < n; at += (int64_t)gridDim.x * (kThreads * kEach)) {
+        Eight<BF16> e[kEach];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, moe::mx_mag(f[k]));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-        const uint32_t byte = moe::mx4_scale_byte(top);
-        q[i] = moe::mx4_pack8(f, byte);
-        if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+        for (int u = 0; u < kEach; ++u) {
+            const int64_t i = at + u * kThreads + threadIdx.x;
+            if (i < n) e[u].template load<STREAM>(x, i);
+        }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int64_t i = at + u * kThreads + threadIdx.x;
+            if (i >= n) continue;
+            float f[8];
+            e[u].values(f);
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, moe::mx_mag(f[k]));
+            top = max(top, (uint32_t)moe::lanes::dpp<moe::lanes::kQuadXor1>((int)top));
+            top = max(top, (uint32_t)moe::lanes::dpp<moe::lanes::kQuadXor2>((int)top));
+            const uint32_t byte = moe::mx4_scale_byte(top);
+            const uint32_t codes = moe::mx4_pack8(f, byte);
+            if (STREAM) __builtin_nontemporal_store(codes, q + i);
+            else q[i] = codes;
+            if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+        }
     }
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(int64_t n, const uint32_t* __restrict__ q,
                                                                   const uint8_t* __restrict__ scales,
                                                                   uint4* __restrict__ x)
 {
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        float f[8];
-        moe::mx4_unpack8(q[i], moe::mx_scale_value(scales[i >> 2]), f);
-        store8<BF16>(x, i, f);
+    for (int64_t at = (int64_t)blockIdx.x * (kThreads * kEach); at < n; at += (int64_t)gridDim.x * (kThreads * kEach)) {
+        uint32_t c[kEach], s[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int64_t i = at + u * kThreads + threadIdx.x;
+            c[u] = i < n ? STREAM ? __builtin_nontemporal_load(q + i) : q[i] : 0u;
+            s[u] = i < n ? scales[i >> 2] : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int64_t i = at + u * kThreads + threadIdx.x;
+            float f[8];
+            moe::mx4_unpack8(c[u], moe::mx_scale_value(s[u]), f);
+            if (i < n) Eight<BF16>::template store<STREAM>(x, i, f);
+        }
     }
 }
 
 int grid_of(int64_t n)
 {
-    const int64_t want = (n + kThreads - 1) / kThreads;
+    const int64_t want = (n + kThreads * kEach - 1) / (kThreads * kEach);
     return (int)(want < kMaxGrid ? want : kMaxGrid);
 }
+// Whether a call's values are more than the caches hold (see mx.h).
+bool past_caches(int64_t n, int dtype) { return n * (dtype == MOE_BF16 ? 16 : 32) > moe::kStreamBytes; }
 
 }  // namespace
 
@@ -83,8 +113,10 @@ hipError_t moe_launch_mx4_quantize(int64_t rows, int64_t cols, int dtype, const 
     const uint4* xv = static_cast<const uint4*>(x);
     uint32_t* qv = static_cast<uint32_t*>(q);
     uint8_t* sv = static_cast<uint8_t*>(scales);
-    if (dtype == MOE_BF16) mx4_quantize_kernel<true><<<grid_of(n), kThreads, 0, st>>>(n, xv, qv, sv);
-    else mx4_quantize_kernel<false><<<grid_of(n), kThreads, 0, st>>>(n, xv, qv, sv);
+    const bool bf = dtype == MOE_BF16;
+    auto* kernel = past_caches(n, dtype) ? (bf ? mx4_quantize_kernel<true, true> : mx4_quantize_kernel<false, true>)
+                                         : (bf ? mx4_quantize_kernel<true, false> : mx4_quantize_kernel<false, false>);
+    kernel<<<grid_of(n), kThreads, 0, st>>>(n, xv, qv, sv);
     return hipGetLastError();
 }
 
@@ -96,7 +128,9 @@ hipError_t moe_launch_mx4_dequantize(int64_t rows, int64_t cols, int dtype, cons
     const uint32_t* qv = static_cast<const uint32_t*>(q);
     const uint8_t* sv = static_cast<const uint8_t*>(scales);
     uint4* xv = static_cast<uint4*>(x);
-    if (dtype == MOE_BF16) mx4_dequantize_kernel<true><<<grid_of(n), kThreads, 0, st>>>(n, qv, sv, xv);
-    else mx4_dequantize_kernel<false><<<grid_of(n), kThreads, 0, st>>>(n, qv, sv, xv);
+    const bool bf = dtype == MOE_BF16;
+    auto* kernel = past_caches(n, dtype) ? (bf ? mx4_dequantize_kernel<true, true> : mx4_dequantize_kernel<false, true>)
+                                         : (bf ? mx4_dequantize_kernel<true, false> : mx4_dequantize_kernel<false, false>);
+    kernel<<<grid_of(n), kThreads, 0, st>>>(n, qv, sv, xv);
     return hipGetLastError();
 }

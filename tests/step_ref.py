@@ -115,8 +115,11 @@ def block_norm_bwd(x, r1, s, r2, alpha, w_post, gate, rows, w_pre, dy, ds):
     g = gate_rows_of(gate, rows, T).to(x.device)
     if gate is not None:
         p, tp = d * n, td * n.abs() + C * (d * n).abs()
-        if rows == 0:
-            out["dgate"] = (p.sum(-1), tp.sum(-1) + chain(H) * U * p.abs().sum(-1))
+        if rows == 0:  # (two sums, as for dx below)
+            big = zero if ds is None else ds.double().abs()
+            if dy is not None:
+                big = big + r2.double()[:, None] * (dyd * w_pre.double()).abs() + r2.double()[:, None] * sh.abs() * ma
+            out["dgate"] = (p.sum(-1), tp.sum(-1) + (chain(H) * U + C) * (n.abs() * big).sum(-1))
         else:
             at = torch.arange(T, device=x.device) // rows
             k = gate.shape[0]
@@ -133,7 +136,13 @@ def block_norm_bwd(x, r1, s, r2, alpha, w_post, gate, rows, w_pre, dy, ds):
     w = w_post.double()
     e, te = dn * w, tdn * w.abs()
     m = (e * xh).mean(-1, keepdim=True)
-    tm = (te * xh.abs()).mean(-1, keepdim=True) + (chain(H) * U + C) * (e * xh).abs().mean(-1, keepdim=True)
+    # the mean is a difference of two sums, of what ds and dy give and of what the
+    # first mean takes away: their terms' magnitudes count, not those of d
+    big = (g * w * xh).abs()
+    parts = zero if ds is None else ds.double().abs()
+    if dy is not None:
+        parts = parts + r2.double()[:, None] * (dyd * w_pre.double()).abs() + r2.double()[:, None] * sh.abs() * ma
+    tm = (te * xh.abs()).mean(-1, keepdim=True) + (chain(H) * U + C) * (big * parts).mean(-1, keepdim=True)
     out["dx"] = (r * (e - xh * m), r * (te + xh.abs() * tm) + C * r * (e.abs() + (xh * m).abs()))
     out["dw_post"] = ((dn * xh).sum(0), (tdn * xh.abs() + C * (dn * xh).abs()).sum(0) + (T + 44) * U * (dn * xh).abs().sum(0))
     return out
