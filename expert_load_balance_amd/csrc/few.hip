@@ -55,6 +55,7 @@ struct Few {
     float *y, *ys;                   // [parts][N][H], [sparts][T][H]
     int32_t *ids, *err, *row_of;
     float *w, *w_out;
+    uint32_t* tables;                // the first kernel's, for the second
     uint16_t* out;
 };
 
@@ -110,6 +111,8 @@ struct Tables {
     int sums[2][kWaves];
     int entries;                     // of routed experts
 };
+constexpr int kTableWords = sizeof(Tables) / 4;
+static_assert(sizeof(Tables) % 4 == 0 && sizeof(Tables) <= moe::kFewTableBytes, "tables");
 struct Choosing {                    // (in the rings' place, before they start)
     uint32_t mask[256];              // tokens that chose the expert
     int16_t base[256];               // its first row
@@ -509,6 +512,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
     __shared__ Reduce red;
     __shared__ __attribute__((aligned(1024))) char rings[kWaves * kRingBytes];
     choose(f, tab, *reinterpret_cast<Choosing*>(rings), blockIdx.x == 0);
+    if (blockIdx.x == 0)   // (the next kernel reads them: 19 us for one token on bf16 weights, 22 where it chooses again)
+        for (int i = threadIdx.x; i < kTableWords; i += kThreads) f.tables[i] = reinterpret_cast<const uint32_t*>(&tab)[i];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
     const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
     const int per = f.F / kTile, sper = f.SF / kTile, entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0;
@@ -554,7 +559,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
     __shared__ Tables tab;
     __shared__ Reduce red;
     __shared__ __attribute__((aligned(1024))) char rings[kWaves * kRingBytes];
-    choose(f, tab, *reinterpret_cast<Choosing*>(rings), false);
+    for (int i = threadIdx.x; i < kTableWords; i += kThreads) reinterpret_cast<uint32_t*>(&tab)[i] = f.tables[i];
+    __syncthreads();
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
     const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
     const int entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0, each = f.H / (2 * kTile);
@@ -710,6 +716,7 @@ hipError_t moe_launch_few(const moe_shape_t& s, const MoeFew& a, char* ws, hipSt
     f.y = reinterpret_cast<float*>(ws + L.y), f.ys = f.y + L.y_shared;
     f.ids = a.ids, f.err = a.err, f.row_of = reinterpret_cast<int32_t*>(ws + L.row_of);
     f.w = reinterpret_cast<float*>(ws + L.w), f.w_out = a.w;
+    f.tables = reinterpret_cast<uint32_t*>(ws + L.tables);
     f.out = static_cast<uint16_t*>(a.out);
     hipError_t e = launch_logits(s, a, logits, st);
     if (e != hipSuccess) return e;

@@ -129,6 +129,7 @@ namespace moe {
 constexpr int kFewMaxH = 8192;   // a wave's part of a row of x stays in registers
 constexpr int kFewPart = 4096;   // values of K of a part of the down projection (h in registers, two bf16 each)
 
+constexpr int kFewTableBytes = 8192; // rows and entries of the choice, at most
 constexpr int kFewLogitK = 1024; // values of H of a part of the router's scores
 constexpr int kFewLogitParts = kFewMaxH / kFewLogitK;
 
@@ -136,10 +137,10 @@ inline int few_logit_parts(int H) { return (H + kFewLogitK - 1) / kFewLogitK; }
 inline int few_unit(int form) { return form == MOE_W_BF16 ? 64 : 128; }
 inline int few_parts(int F) { return (F + kFewPart - 1) / kFewPart; }
 
-// logits [parts][T][E], the router's w [N] and each assignment's row [N], h in two bf16
+// logits [parts][T][E], the router's w [N], each assignment's row [N], the choice's tables, h in two bf16
 // planes [N][F] + [T][shared_F], y fp32 [parts][N][H] + [shared parts][T][H]
 struct FewWsLayout {
-    size_t logits, w, row_of, h, y, total;
+    size_t logits, w, row_of, tables, h, y, total;
     size_t h_shared, h_plane;   // elements: where the shared expert's rows begin, and the second plane
     size_t y_shared;            // elements
 };
@@ -151,6 +152,7 @@ inline FewWsLayout few_ws_layout(const moe_shape_t& s, int shared_F)
     w.logits = o; o = align256(o + ((size_t)few_logit_parts(s.H) * s.T * s.E + 1) * 4);
     w.w = o;      o = align256(o + n1 * 4);
     w.row_of = o; o = align256(o + n1 * 4);
+    w.tables = o; o = align256(o + kFewTableBytes);
     w.h_shared = N * s.F;
     w.h_plane = w.h_shared + (size_t)s.T * shared_F;
     w.h = o;      o = align256(o + 2 * w.h_plane * 2);
