@@ -559,7 +559,8 @@ struct Geo {
     // rows (a stage takes two), the scales of up to four stages (16 bytes for
     // each weight row, then for each row), the lists.
     // (The scales of a stage of 256 values come as 16 bytes a row, with those of
-    // its neighbour: one copy instruction costs as much for 4 bytes a row.)
+    // its neighbour, in every other stage: 128 x 16 rows of 4096 x 1536, gate/up 189
+    // -> 183 us, down 91 -> 88.)
     static constexpr int kSlot = KIND == 0 ? kA : kA + kWBytes;
     static constexpr int kScaleRow = KIND == 0 || kPanels == 2 ? 16 : 4;
     static constexpr int kScale = (kTN + kRows) * kScaleRow;
@@ -702,7 +703,7 @@ struct Copier {
     // Of 4-bit weights the compiler keeps the stage in a vector register.
     __device__ __forceinline__ static int held(int v) { return WB == 8 ? v : uni(v); }
     // The next stage into a slot; each call of row and weight is one
-    // instruction, scales is two.
+    // instruction, scales is two or none.
     __device__ __forceinline__ void row(int i, uint32_t slot, int wave) const
     {
         if constexpr (GE::kPanels == 1) {
@@ -722,6 +723,13 @@ struct Copier {
         copy16<STREAM>(buffer_of(i < kHalf ? wb0 : wb1, i < kHalf || MODE == kGateUp || upper > 0 ? range() : 0u), off,
                held(at), unit + wave * 1024);
     }
+    // Whether the next stage's copies have scales: of stages of 256 values the even
+    // ones and a unit's first (a unit that starts elsewhere than at 0 keeps their
+    // order, so an odd stage follows the even one whose copy holds its scales).
+    __device__ __forceinline__ bool scaled() const
+    {
+        return GE::kPanels == 1 || (st < real && (st == 0 || ((k0 + ks()) & 1) == 0));
+    }
     __device__ __forceinline__ void scales(uint32_t sslot, int wave, int lane) const
     {
         if constexpr (GE::kPanels == 1) {
@@ -729,9 +737,9 @@ struct Copier {
             if (lane < GE::kRows / 4) copy4(buffer_of(asb, range()), asoff, ks() * 4, sslot + kTN * 4 + wave * GE::kRows);
         } else {  // 512 values' worth, of which the stage's are the first or the second half
             const int at = held((k0 + ks()) / 2 * 16);
-            copy16(buffer_of(sb, st < real ? wrange : 0u), wsoff, at, sslot + wave * 1024);
-            if (lane < GE::kRows / 4)
-                copy16(buffer_of(asb, st < real ? arange : 0u), asoff, at, sslot + kTN * 16 + wave * GE::kRows * 4);
+            if (!scaled()) return;
+            copy16(buffer_of(sb, wrange), wsoff, at, sslot + wave * 1024);
+            if (lane < GE::kRows / 4) copy16(buffer_of(asb, arange), asoff, at, sslot + kTN * 16 + wave * GE::kRows * 4);
         }
     }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
@@ -867,6 +875,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     Copier<MODE, KIND, WEIGHTS, WB> cp;
     cp.setup(g, u, list(0), wave, lane);
     int m = 0;       // this unit's number
+    int with = 0;    // whether the last stage copied came with scales
     int at = 0;      // slot of the stage being computed
     int to = 0;      // slot of the next copies
     auto copy_next = [&]() {
@@ -874,6 +883,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
             if (more) cp.setup(again(), un, list(m + 1), wave, opaque_v(lane));
             else cp.nothing();
         }
+        with = cp.scaled();
         cp.stage(lds_u + (uint32_t)to * GE::kSlot, lds_u + GE::kScale0 + (uint32_t)to * GE::kScale, wave, lane);
         to = to + 1 == GE::kSlots ? 0 : to + 1;
     };
@@ -899,11 +909,14 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                 cut = uni(cut < 0 ? cut + u.KT : cut);
             }
         }
+        uint32_t wnext[2][2], tnext[2][GE::TB];  // [panel]: the odd stage's scales, from the even one
         for (int s = 0; s < KT; ++s) {
             // this stage landed in this wave: the copies of the kAhead - 1
             // stages after it may be out (a list or stores among them only
             // make the wait longer)
-            wait_vm_lgkm<(GE::kAhead - 1) * GE::kPerStage>();
+            static_assert(GE::kPanels == 1 || GE::kAhead <= 2, "the stage after this one is the last copied");
+            if (GE::kPanels == 2 && GE::kAhead == 2 && !uni(with)) wait_vm_lgkm<GE::kPerStage - 2>();
+            else wait_vm_lgkm<(GE::kAhead - 1) * GE::kPerStage>();
             slot_barrier();  // ... in every wave; the slot of the stage before is free
             if (s == 0) {
                 // the unit after next: its list goes to the place of the list
@@ -921,18 +934,44 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
             const char* slot = lds + at * GE::kSlot;
             const char* ssl = lds + GE::kScale0 + at * GE::kScale;
             at = at + 1 == GE::kSlots ? 0 : at + 1;
+            uint32_t wnow[2][2], tnow[2][GE::TB];
+            if constexpr (GE::kPanels == 2) {
+                const bool odd = (u.k0 + s) & 1;
+                if (odd && s > 0) {
+                    // (past the unit's last stage they are the next rows', maybe NaN, on codes of 0)
+                    const uint32_t keep = s < u.KT ? ~0u : 0u;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) wnow[p][q] = wnext[p][q] & keep;
+#pragma unroll
+                        for (int b = 0; b < GE::TB; ++b) tnow[p][b] = tnext[p][b] & keep;
+                    }
+                } else {
+                    auto read = [&](int row, uint32_t& n0, uint32_t& n1, uint32_t& x0, uint32_t& x1) {
+                        const u32x4 w = *reinterpret_cast<const u32x4*>(ssl + row * 16);
+                        n0 = odd ? w[2] : w[0];
+                        n1 = odd ? w[3] : w[1];
+                        x0 = w[2];
+                        x1 = w[3];
+                    };
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) read(GE::wrow(wn, q) + fr, wnow[0][q], wnow[1][q], wnext[0][q], wnext[1][q]);
+#pragma unroll
+                    for (int b = 0; b < GE::TB; ++b) read(kTN + 32 * b + fr, tnow[0][b], tnow[1][b], tnext[0][b], tnext[1][b]);
+                }
+            }
 #pragma unroll
             for (int p = 0; p < GE::kPanels; ++p) {
                 // 128 values of K: the four blocks' scales of each weight and row
-                const int so = GE::kPanels == 1 ? 0 : ((u.k0 + s) & 1) * 8 + 4 * p;
                 const char *const rows = slot + p * (GE::kRows * kTK), *const weights = slot + GE::kA;
                 uint32_t ws[2], ts[GE::TB];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    ws[q] = *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * GE::kScaleRow + so);
+                    ws[q] = GE::kPanels == 2 ? wnow[p][q] : *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * 4);
 #pragma unroll
                 for (int b = 0; b < GE::TB; ++b)
-                    ts[b] = *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * GE::kScaleRow + so);
+                    ts[b] = GE::kPanels == 2 ? tnow[p][b] : *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * 4);
                 if (GE::kPanels == 2 && p == 1) {
                     // (past a row's end the scales are the next row's, maybe NaN, on codes of 0)
                     const uint32_t keep = s == cut ? 0u : ~0u;

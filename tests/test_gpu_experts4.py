@@ -189,3 +189,23 @@ def test_bf16_layer_on_dequantised_weights_agrees():
             want[t] += w[t, j].double() * ((h * torch.sigmoid(h) * (xd[t] @ U.t())) @ D.t())
     # two roundings to e4m3 (2^-4 of a value at most, 0.026 of the norm at random), and bf16's
     assert float((L.out.double() - want).norm() / want.norm()) < 0.07
+
+
+@pytest.mark.parametrize("T", [20, 90, 400])
+@pytest.mark.parametrize("F", [128, 256, 384, 512])
+def test_a_nan_block_beside_short_rows(T, F):
+    """Rows of one and two stages: the bytes behind a row's scales are other rows'."""
+    H, E = 256, 2
+    g = gen(H + F + T)
+    L = MoeLayerMx(moe.Shape(T, H, E, 1, F, 1, 0, moe.MOE_BF16), DEV, weight_bits=4)
+    xq, xs = quantized(randn(g, T, H))
+    ids, w = choose(g, T, E, 1, 0.0)
+    wts = weights4(g, E, F, H)
+    run(L, xq, xs, ids, w, wts)
+    check(L, xq, xs, ids, wts)
+    want, on = L.out.clone(), ids[:, 0] == 0
+    wts[2][1][0, 70:73] = 255
+    run(L, xq, xs, ids, w, wts)
+    cols = [c for c in range(H) if not 70 <= c < 73]
+    assert bool(torch.isnan(L.out[on][:, 70:73]).all())
+    assert torch.equal(L.out[on][:, cols], want[on][:, cols]) and torch.equal(L.out[~on], want[~on])
