@@ -52,6 +52,7 @@
 // registers, held across a tile's stages for the code between tiles; the stages'
 // own addresses are not among them. The down kernels keep 20 bytes a lane in scratch.
 #include <type_traits>
+#include <utility>
 
 #include "lds_pipe.h"
 #include "step.h"
@@ -742,6 +743,20 @@ struct Copier {
             if (lane < GE::kRows / 4) copy16(buffer_of(asb, arange), asoff, at, sslot + kTN * 16 + wave * GE::kRows * 4);
         }
     }
+    // The same in pieces, in the same order: weights, rows, scales.
+    template <int I>
+    __device__ __forceinline__ void piece(uint32_t slot, uint32_t sslot, int wave, int lane)
+    {
+        if constexpr (I < GE::kWCopies) {
+            if (WEIGHTS == kStreamed || (WEIGHTS == kByExpert && alone)) weight<true>(I, slot + GE::kA + I * 4096, wave);
+            else weight<false>(I, slot + GE::kA + I * 4096, wave);
+        } else if constexpr (I < GE::kWCopies + GE::kACopies) {
+            row(I - GE::kWCopies, slot, wave);
+        } else {
+            scales(sslot, wave, lane);
+            ++st;
+        }
+    }
     __device__ __forceinline__ void stage(uint32_t slot, uint32_t sslot, int wave, int lane)
     {
         if (WEIGHTS == kStreamed || (WEIGHTS == kByExpert && alone)) {
@@ -830,6 +845,15 @@ __device__ __forceinline__ void store_part(const Gemm& g, const Unit& u, int i,
 // Bound by streaming the weights: a ring of up to four stages, one barrier per
 // stage, the fragments read as the products need them. 128 experts of 16 rows
 // of 4096 x 1536: 6.1 TB/s of weights, where a plain read of 4 GB reaches 6.2.
+template <int I>
+using Number = std::integral_constant<int, I>;
+// f(0), f(1), ... with the number as a constant.
+template <typename F, int... J>
+__device__ __forceinline__ void unrolled(F f, std::integer_sequence<int, J...>)
+{
+    (f(Number<J>{}), ...);
+}
+
 template <int MODE, int KIND, Weights WEIGHTS, int WB>
 __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id)
 {
@@ -846,7 +870,7 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     // of exponent 8 and more and the others: the products of a part differ by 10
     // binades at most, of which the cut takes 9. The time for a stage is half, and
     // the widening's conversions would show: 128 x 16 rows of 4096 x 1536, gate/up
-    // 164 us in one part, 203 in bf16.
+    // 160 us in one part, 181 in two, 203 in bf16.
     constexpr bool kWide = WB == 8 && MODE == kGateUp && KIND >= 2, kSplit = WB == 4 && MODE == kGateUp && KIND >= 2;
     const KindWork work = work_of<MODE, WB>(g, KIND);
     const int end = work.first + work.count, P = g.P;
@@ -878,12 +902,15 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
     int with = 0;    // whether the last stage copied came with scales
     int at = 0;      // slot of the stage being computed
     int to = 0;      // slot of the next copies
-    auto copy_next = [&]() {
+    auto next_unit = [&]() {
         if (cp.st == cp.KT) {
             if (more) cp.setup(again(), un, list(m + 1), wave, opaque_v(lane));
             else cp.nothing();
         }
         with = cp.scaled();
+    };
+    auto copy_next = [&]() {
+        next_unit();
         cp.stage(lds_u + (uint32_t)to * GE::kSlot, lds_u + GE::kScale0 + (uint32_t)to * GE::kScale, wave, lane);
         to = to + 1 == GE::kSlots ? 0 : to + 1;
     };
@@ -930,7 +957,21 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                     copy_list<KIND>(ga, u2, list_u(m + 2), wave, lane);
                 }
             }
-            copy_next();
+            // (4-bit weights: the rows' and the scales' copies go out beside the products, whose
+            // operands have all been read: 128 experts of 16, 50 and 100 rows of 4096 x 1536,
+            // gate/up and down, 252 -> 246, 360 -> 333 and 386 -> 370 us)
+            const uint32_t cslot = lds_u + (uint32_t)to * GE::kSlot, csslot = lds_u + GE::kScale0 + (uint32_t)to * GE::kScale;
+            auto pieces = [&](auto from, auto count) {
+                unrolled([&](auto i) { cp.template piece<decltype(from)::value + decltype(i)::value>(cslot, csslot, wave, lane); },
+                         std::make_integer_sequence<int, decltype(count)::value>{});
+            };
+            if constexpr (GE::kPanels == 2) {
+                next_unit();
+                to = to + 1 == GE::kSlots ? 0 : to + 1;
+                pieces(Number<0>{}, Number<GE::kWCopies>{});
+            } else {
+                copy_next();
+            }
             const char* slot = lds + at * GE::kSlot;
             const char* ssl = lds + GE::kScale0 + at * GE::kScale;
             at = at + 1 == GE::kSlots ? 0 : at + 1;
@@ -961,25 +1002,60 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
                     for (int b = 0; b < GE::TB; ++b) read(kTN + 32 * b + fr, tnow[0][b], tnow[1][b], tnext[0][b], tnext[1][b]);
                 }
             }
+            if constexpr (GE::kPanels == 2) {
+                constexpr int S = kSplit ? 2 : 1, kMfmas = 4 * GE::TB * 2 * S, kLeft = GE::kACopies + 1;
+                const char *const weights = slot + GE::kA;
+                i32x8 wf[4][2], tf[4][GE::TB], low;
 #pragma unroll
-            for (int p = 0; p < GE::kPanels; ++p) {
+                for (int k = 0; k < 4; ++k) {
+                    const int c0 = ((4 * (k % 2) + half) ^ swz(fr)) * 16, c1 = ((4 * (k % 2) + 2 + half) ^ swz(fr)) * 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        wf[k][i] = wfrag<4>(weights + (GE::wrow(wn, i) + fr) * GE::kWRow + ((2 * k + half) ^ swz(fr)) * 16, weights);
+#pragma unroll
+                    for (int b = 0; b < GE::TB; ++b) {
+                        const char* t = slot + k / 2 * (GE::kRows * kTK) + (32 * b + fr) * 128;
+                        tf[k][b] = frag(t + c0, t + c1);
+                    }
+                }
+                // this lane's blocks: bytes 0 and 2 of the words, 1 and 3 in the upper lanes
+                // (past a row's end the scales are the next row's, maybe NaN, on codes of 0)
+                const uint32_t keep = s == cut ? 0u : ~0u;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) wnow[p][q] = (p ? wnow[p][q] & keep : wnow[p][q]) >> 8 * half;
+#pragma unroll
+                    for (int i = 0; i < GE::TB; ++i) tnow[p][i] = (p ? tnow[p][i] & keep : tnow[p][i]) >> 8 * half;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                unrolled([&](auto n_tag) {
+                    constexpr int n = decltype(n_tag)::value, q = n % 2, sp = n / 2 % S, b = n / (2 * S) % GE::TB;
+                    constexpr int k = n / (2 * S * GE::TB), p = k / 2;
+                    if constexpr (kSplit && n % (2 * S) == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int up = (int)upper_codes((uint32_t)tf[k][b][i]);
+                            low[i] = tf[k][b][i] ^ up;
+                            tf[k][b][i] = up;
+                        }
+                    }
+                    acc[b][q] = mfma<4, 2 * (k % 2)>(wf[k][q], sp ? low : tf[k][b], acc[b][q], wnow[p][q], tnow[p][b]);
+                    constexpr int from = n * kLeft / kMfmas, upto = (n + 1) * kLeft / kMfmas;
+                    if constexpr (upto > from) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        pieces(Number<GE::kWCopies + from>{}, Number<upto - from>{});
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }, std::make_integer_sequence<int, kMfmas>{});
+            } else {
                 // 128 values of K: the four blocks' scales of each weight and row
-                const char *const rows = slot + p * (GE::kRows * kTK), *const weights = slot + GE::kA;
+                const char *const rows = slot, *const weights = slot + GE::kA;
                 uint32_t ws[2], ts[GE::TB];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    ws[q] = GE::kPanels == 2 ? wnow[p][q] : *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * 4);
+                for (int q = 0; q < 2; ++q) ws[q] = *reinterpret_cast<const uint32_t*>(ssl + (GE::wrow(wn, q) + fr) * 4);
 #pragma unroll
-                for (int b = 0; b < GE::TB; ++b)
-                    ts[b] = GE::kPanels == 2 ? tnow[p][b] : *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * 4);
-                if (GE::kPanels == 2 && p == 1) {
-                    // (past a row's end the scales are the next row's, maybe NaN, on codes of 0)
-                    const uint32_t keep = s == cut ? 0u : ~0u;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) ws[q] &= keep;
-#pragma unroll
-                    for (int b = 0; b < GE::TB; ++b) ts[b] &= keep;
-                }
+                for (int b = 0; b < GE::TB; ++b) ts[b] = *reinterpret_cast<const uint32_t*>(ssl + (kTN + 32 * b + fr) * 4);
                 if constexpr (kWide) {
                     auto block = [&](auto b_tag) {  // 32 values of K, 16 per half of the wave
                         constexpr int B = decltype(b_tag)::value;
@@ -1015,27 +1091,15 @@ __device__ __forceinline__ void ring_tiles(const Gemm& g, char* lds, int slot_id
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const char* w = weights + (GE::wrow(wn, q) + fr) * GE::kWRow;
-                            if constexpr (WB == 8) wf[q] = wfrag<8>(w + c0, w + c1);
-                            else wf[q] = wfrag<4>(w + ((4 * p + 2 * KK + half) ^ swz(fr)) * 16, w);
+                            wf[q] = frag(w + c0, w + c1);
                         }
 #pragma unroll
                         for (int b = 0; b < GE::TB; ++b) {
                             const char* t = rows + (32 * b + fr) * 128;
-                            i32x8 tf = frag(t + c0, t + c1), low;
-                            if constexpr (kSplit)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int up = (int)upper_codes((uint32_t)tf[i]);
-                                    low[i] = tf[i] ^ up;
-                                    tf[i] = up;
-                                }
+                            const i32x8 tf = frag(t + c0, t + c1);
 #pragma unroll
                             for (int q = 0; q < 2; ++q)
-                                acc[b][q] = mfma<WB, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
-                            if constexpr (kSplit)
-#pragma unroll
-                                for (int q = 0; q < 2; ++q)
-                                    acc[b][q] = mfma<WB, 2 * KK>(wf[q], low, acc[b][q], ws[q], ts[b]);
+                                acc[b][q] = mfma<8, 2 * KK>(wf[q], tf, acc[b][q], ws[q], ts[b]);
                         }
                     };
                     kstep(std::integral_constant<int, 0>{});
