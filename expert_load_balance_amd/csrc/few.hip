@@ -20,6 +20,14 @@
 // h = silu(g) u is kept as two bf16 (value and remainder), so that it carries 16
 // bits into the down projection; its sums are kept in fp32 for each assignment
 // and added in j order.
+//
+// Measured (us and TB/s of weights, two layers in turn): one token, 8 of 128 experts,
+// 4096 x 1536, bf16: scores 4.7, gate/up 36 (5.5), down 19 (5.2), combine 4.6; five
+// tokens, top-2 of 8, 4096 x 14336, 8-bit: gate/up 113 (6.4), down 60 (6.2); sixteen
+// tokens, top-8 of 256 and a shared expert, 7168 x 2048, 4-bit: gate/up 255 (6.4), down
+// 148 (5.5: a wave has a single unit of a row, and every step of 32 rows a barrier).
+// All in one launch, with shares of the steps drawn from counters and waits of the
+// workgroups for each other's h and y, took 81 us where these four kernels take 64.
 #include <type_traits>
 
 #include "lanes.h"
@@ -251,7 +259,8 @@ __device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
 // row r's chunks of 16 bytes 2 g and 2 g + 1. In LDS a row's chunks are turned so
 // that lanes of 16 rows read different banks (see lds_pipe.h). kWords: of four
 // scales, of a row's unit. (A unit of 64 bytes of 4-bit codes was slower, whether the
-// copies were kept in the caches or not: 307 and 352 us where this takes 280.)
+// copies were kept in the caches or not: 307 and 352 us where this takes 257. Chunks g and g + 4 to a
+// lane, which bring fewer conflicts in the LDS, took the same time.)
 template <int FORM>
 struct Form;
 template <>

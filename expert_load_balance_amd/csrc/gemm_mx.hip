@@ -1,4 +1,5 @@
-// gemm_mx.hip -- the grouped SwiGLU expert GEMM on 8-bit blocks (serving).
+// gemm_mx.hip -- the grouped SwiGLU expert GEMM on 8-bit blocks (serving), with
+// weights in 8-bit or 4-bit blocks (WB).
 //
 //   gate/up: h = blocks(silu(Wg a) * (Wu a)), 32 columns of h to a scale;
 //   down:    y = Wd h, rounded to bf16.
@@ -46,6 +47,14 @@
 // stages a tile hide neither its cold start nor its epilogue, which takes 5 to 7 us a
 // tile: the vector unit's silu and quantisation of 128 values a lane in gate/up
 // (whose 32 KB of a tile are no load on the memory), y's writes in down.
+//
+// 4-bit weights (half the bytes; the instruction takes as long, an 8-bit operand sets
+// its rate):
+//   2048 rows of 128 experts, 4096 x 1536 176 and 87    (4.9 TB/s of weights)
+//   4094 rows of 8 experts, 4096 x 14336  412 and 220   (2.33 and 2.19 PFLOP/s)
+//   65536 rows of 256 experts, 7168 x 2048 1860 and 1115 (2.07 and 1.73 PFLOP/s)
+// The first is bound by what a stage of a small tile does in turn (copies out, reads,
+// splitting the rows' codes, products) on one wave a SIMD.
 //
 // Registers: the 256-row kernels fill the vector registers (243 and 251 and 256
 // accumulators) and spill 128 (gate/up) and 116 (down) scalars to lanes of vector

@@ -135,8 +135,8 @@ typedef struct moe_few_weights {
 /* Most tokens of moe_few_layer. */
 #define MOE_FEW_TOKENS 32
 
-/* Bytes of device workspace moe_few_layer needs (logits, the activations h,
- * counters, partial sums). shared_F: width of the shared expert, 0 without one. 0 on a
+/* Bytes of device workspace moe_few_layer needs (scores, the choice,
+ * the activations h, partial sums). shared_F: width of the shared expert, 0 without one. 0 on a
  * shape that moe_few_layer refuses. Calls that may run at the same time, and
  * captured graphs that may, need a workspace each. */
 size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t shared_F);
