@@ -152,8 +152,8 @@ size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t s
  * tokens. No plan, no dispatch: R and S of the shape are not used.
  *   shape: dtype MOE_BF16; form a moe_weight_form_t, for the routed and the
  *   shared experts; MOE_W_MX8 and MOE_W_MX4 need H, F and shared_F multiples
- *   of 128, MOE_W_BF16 of 64; H <= 8192; else, and for more tokens or another
- *   dtype, MOE_EUNSUPPORTED;
+ *   of 128, MOE_W_BF16 of 64; H <= 8192; H * F and H * shared_F below 2^31 - 64;
+ *   else, and for more tokens or another dtype, MOE_EUNSUPPORTED;
  *   d_x bf16[T][H]; d_w_router bf16[E][H]; d_bias float[E] or NULL; h_routed:
  *   host memory, read before the call returns; h_shared with one expert of
  *   width shared_F, or NULL with shared_F 0; d_out bf16[T][H]; d_ids
