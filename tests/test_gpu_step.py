@@ -342,3 +342,11 @@ def test_mx4_every_code_and_scale():
         w = ref.values4(q, s).to(t)
         assert torch.equal(torch.isnan(v), torch.isnan(w)), t
         assert torch.equal(v[:255], w[:255]), t
+
+
+@pytest.mark.parametrize("case", [(5, 640, BF, 0, True, False, True), (3, 32832, BF, 0, True, False, True),
+                                  (6, 20000, F32, 0, False, False, True), (5, 640, F32, 0, True, False, False),
+                                  (64, 8192, BF, 7, True, True, True), (515, 4100, F32, 0, True, True, True)], ids=ident)
+def test_a_gate_without_a_norm_behind_and_wide_rows(case):
+    test_block_norm(case)
+    test_block_norm_backward(case)
