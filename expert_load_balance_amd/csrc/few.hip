@@ -3,9 +3,10 @@
 //   logits = x Wr^T; top-k of logits + bias; w = softmax of the chosen logits;
 //   out = sum_j w_j Wd (silu(Wg x) * (Wu x)) (+ the shared expert).
 //
-// Bound by the live experts' weights, each read once. A step is 16 weight rows
+// Bound by the live experts' weights, each read once (few_two_tiles says where an
+// expert with more than 16 rows reads them again). A step is 16 weight rows
 // of two streams (gate and up; in the down projection, two neighbours) times up
-// to 16 rows of one expert, on v_mfma_f32_16x16x32_bf16 (codes are widened to
+// to 16 rows of one expert, or 32, on v_mfma_f32_16x16x32_bf16 (codes are widened to
 // bf16, exactly); the rows' values stay in registers from step to step. The eight
 // waves of a workgroup share K; each brings its own weights through a ring of
 // copies in LDS that runs across steps (12 to 14 KB in flight a wave), and their
@@ -44,7 +45,7 @@ using moe::lds::uni_ptr;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr int kTile = 16;                                      // rows of an entry
+constexpr int kTile = moe::kFewTile;                            // rows of a product
 constexpr int kMaxAssign = MOE_FEW_TOKENS * 64;                // k is at most 64
 constexpr int kMaxEntries = 256 + kMaxAssign / (kTile + 1) + 1; // experts, and second tiles of those above 16 rows
 
@@ -52,6 +53,7 @@ constexpr int kMaxEntries = 256 + kMaxAssign / (kTile + 1) + 1; // experts, and 
 // rows N .. N + T - 1 the shared expert's.
 struct Few {
     int T, H, E, k, F, SF, N;
+    bool two_tiles;                  // entries of up to 32 rows
     int planes;                      // of the router's scores
     int parts, sparts;               // of K in the down projection
     const uint16_t* x;
@@ -114,10 +116,11 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(int T, int H, int 
 // -------------------------------------------------------------- the choice --
 struct Tables {
     uint8_t tok[kMaxAssign];         // token of a row
-    int16_t entry_e[kMaxEntries], entry_row[kMaxEntries];
-    uint8_t entry_n[kMaxEntries];
-    int sums[2][kWaves];
-    int entries;                     // of routed experts
+    // runs of up to 16 rows of one expert, and the experts with rows (of up to 32)
+    int16_t entry_e[kMaxEntries], entry_row[kMaxEntries], live_e[256], live_row[256];
+    uint8_t entry_n[kMaxEntries], live_n[256];
+    int sums[3][kWaves];
+    int entries, live;
 };
 constexpr int kTableWords = sizeof(Tables) / 4;
 static_assert(sizeof(Tables) % 4 == 0 && sizeof(Tables) <= moe::kFewTableBytes, "tables");
@@ -149,7 +152,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 }
 
 // Top-k of every token (a wave takes tokens wave, wave + 8, ...), then the
-// experts' rows and the entries: runs of up to 16 rows of one expert.
+// experts' rows and the entries.
 __device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -217,21 +220,24 @@ __device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
     __syncthreads();
     // rows and entries before each expert (threads 0 .. 255 hold one each)
     const int n = tid < 256 ? __popc(c.mask[tid]) : 0, tiles = (n + kTile - 1) / kTile;
-    int rows_to = n, tiles_to = tiles;
+    int rows_to = n, tiles_to = tiles, live_to = n > 0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int a = __shfl_up(rows_to, off), b = __shfl_up(tiles_to, off);
+        const int a = __shfl_up(rows_to, off), b = __shfl_up(tiles_to, off), l = __shfl_up(live_to, off);
         rows_to += lane >= off ? a : 0;
         tiles_to += lane >= off ? b : 0;
+        live_to += lane >= off ? l : 0;
     }
     if (lane == 63) {
         s.sums[0][wave] = rows_to;
         s.sums[1][wave] = tiles_to;
+        s.sums[2][wave] = live_to;
     }
     __syncthreads();
     for (int w = 0; w < wave; ++w) {
         rows_to += s.sums[0][w];
         tiles_to += s.sums[1][w];
+        live_to += s.sums[2][w];
     }
     if (tid < 256) {
         c.base[tid] = (int16_t)(rows_to - n);
@@ -241,8 +247,16 @@ __device__ void choose(const Few& f, Tables& s, Choosing& c, bool tell)
             s.entry_row[at] = (int16_t)(rows_to - n + i * kTile);
             s.entry_n[at] = (uint8_t)min(kTile, n - i * kTile);
         }
+        if (n > 0) {
+            s.live_e[live_to - 1] = (int16_t)tid;
+            s.live_row[live_to - 1] = (int16_t)(rows_to - n);
+            s.live_n[live_to - 1] = (uint8_t)n;
+        }
     }
-    if (tid == kThreads - 1) s.entries = tiles_to;
+    if (tid == kThreads - 1) {
+        s.entries = tiles_to;
+        s.live = live_to;
+    }
     __syncthreads();
     for (int i = tid; i < f.N; i += kThreads) {
         const int t = i / f.k, e = c.id[i];
@@ -344,7 +358,8 @@ __device__ __forceinline__ void unrolled(F f, std::integer_sequence<int, J...>)
     (f(std::integral_constant<int, J>{}), ...);
 }
 
-// The waves' sums of one step, [wave][stream][lane], doubled.
+// The waves' sums of one step, [wave][stream][lane], doubled (for two steps in turn, or
+// the two tiles of a step).
 struct Reduce {
     f32x4 v[2][kWaves][2][64];
 };
@@ -353,10 +368,10 @@ struct Reduce {
 // entry's first weight row (stream 1: up, or 16 rows on), `rows` of them, of K
 // values; step_rows weight rows from a step to the next; u0, cnt: this
 // wave's units of K. load(b) fetches the rows' values of those units (NB 2: and
-// their remainders). ring: the wave's LDS. done(step, sums of both streams) is
-// called by 256 threads: thread e has weight row e / 64 % 4 * 4 + e % 4 of the
-// step's and the entry's row e / 4 % 16.
-template <int FORM, int NU, int NB, typename Load, typename Done>
+// their remainders; TB 2: of both tiles of 16 rows). ring: the wave's LDS. done(step,
+// sums of both streams, tile) is called by 256 threads of a tile: thread e has weight
+// row e / 64 % 4 * 4 + e % 4 of the step's and the tile's row e / 4 % 16.
+template <int FORM, int NU, int TB, int NB, typename Load, typename Done>
 __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const uint8_t* const (&sc)[2], int K, int rows, int step_rows,
                                           int u0, int cnt, int s0, int s1, const char* ring, Load load, Reduce& red,
                                           int& turn, Done done)
@@ -424,13 +439,15 @@ __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const ui
     };
 #pragma unroll
     for (int j = 0; j < D; ++j) issue(s0 + j / I, j % I);
-    bf16x8 b[NB][NU * kLoads * FM::kSub];
+    bf16x8 b[TB][NB][NU * kLoads * FM::kSub];
     load(b);
     landed<0>();
     read();
     read_scales();
     for (int s = s0; s < s1; ++s) {
-        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        f32x4 acc[TB][2];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
         float f[2][NU][FM::kWords == 2 ? 2 : 1];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -455,34 +472,40 @@ __device__ __forceinline__ void run_steps(const uint8_t* const (&w)[2], const ui
 #pragma unroll
                 for (int q = 0; q < FM::kSub; ++q)
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b[n][(u * kLoads + i) * FM::kSub + q], acc[m], 0, 0, 0);
+                    for (int t = 0; t < TB; ++t)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b[t][n][(u * kLoads + i) * FM::kSub + q], acc[t][m], 0, 0, 0);
             }
         }, std::make_integer_sequence<int, I>{});
-        red.v[turn][wave][0][lane] = acc[0];
-        red.v[turn][wave][1][lane] = acc[1];
+        if (TB == 2) moe::lds::slot_barrier();  // (the step before's sums have been read)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) red.v[TB == 2 ? t : turn][wave][m][lane] = acc[t][m];
         moe::lds::wait_vm_lgkm<63>();  // the sums are in LDS; copies stay in flight
         moe::lds::slot_barrier();
-        // one half of the waves adds them up, the other goes on, in turns: a value of
-        // each stream a thread, in the waves' order
-        if ((wave >> 2) == (s & 1)) {
-            const int e = threadIdx.x & 255;
+        // one half of the waves adds them up, the other goes on, in turns (or each half
+        // a tile): a value of each stream a thread, in the waves' order
+        if (TB == 2 || (wave >> 2) == (s & 1)) {
+            const int e = threadIdx.x & 255, from = TB == 2 ? wave >> 2 : turn;
             float x[kWaves], y[kWaves];
 #pragma unroll
             for (int v = 0; v < kWaves; ++v) {
-                x[v] = reinterpret_cast<const float*>(red.v[turn][v][0])[e];
-                y[v] = reinterpret_cast<const float*>(red.v[turn][v][1])[e];
+                x[v] = reinterpret_cast<const float*>(red.v[from][v][0])[e];
+                y[v] = reinterpret_cast<const float*>(red.v[from][v][1])[e];
             }
 #pragma unroll
             for (int v = 1; v < kWaves; ++v) {
                 x[0] += x[v];
                 y[0] += y[v];
             }
-            done(s, x[0], y[0]);
+            done(s, x[0], y[0], TB == 2 ? wave >> 2 : 0);
         }
         turn ^= 1;
     }
     landed<0>();  // copies of nothing past the last step
+    if (TB == 2) moe::lds::slot_barrier();  // (the next entry's sums may have one tile: no barrier before they are written)
 }
 
 // Values of an entry's rows as operands: lane (n, g) takes of row n, at `row`, of
@@ -513,7 +536,8 @@ __device__ __forceinline__ void my_run(int64_t total, int& a, int& z)
 }
 
 // ---------------------------------------------------------------- gate, up --
-template <int FORM, int NU>
+// TB: tiles of 16 rows that an entry has at most.
+template <int FORM, int NU, int TB>
 __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
 {
     using FM = Form<FORM>;
@@ -525,7 +549,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
         for (int i = threadIdx.x; i < kTableWords; i += kThreads) f.tables[i] = reinterpret_cast<const uint32_t*>(&tab)[i];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
     const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
-    const int per = f.F / kTile, sper = f.SF / kTile, entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0;
+    const int per = f.F / kTile, sper = f.SF / kTile, entries = uni(TB == 2 ? tab.live : tab.entries), sentries = f.SF ? (f.T + TB * kTile - 1) / (TB * kTile) : 0;
     const int units = (f.H + FM::kUnit - 1) / FM::kUnit, u0 = uni(wave * units / kWaves), cnt = uni((wave + 1) * units / kWaves) - u0;
     const char* ring = rings + wave * kRingBytes;
     int at, end, turn = 0;
@@ -534,34 +558,42 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
         const bool shared = at >= entries * per;
         const int local = shared ? at - entries * per : at, each = shared ? sper : per;
         const int entry = uni(local / each), s0 = local - entry * each, s1 = min(each, s0 + end - at);
-        const int e = shared ? 0 : uni((int)tab.entry_e[entry]);
-        const int row0 = shared ? entry * kTile : uni((int)tab.entry_row[entry]);
-        const int rows = shared ? min(kTile, f.T - row0) : uni((int)tab.entry_n[entry]);
+        const int e = shared ? 0 : uni((int)(TB == 2 ? tab.live_e : tab.entry_e)[entry]);
+        const int row0 = shared ? entry * TB * kTile : uni((int)(TB == 2 ? tab.live_row : tab.entry_row)[entry]);
+        const int rows = shared ? min(TB * kTile, f.T - row0) : uni((int)(TB == 2 ? tab.live_n : tab.entry_n)[entry]);
         const size_t first = (size_t)e * f.F;
         const uint8_t* const w[2] = {(shared ? f.sgate : f.gate) + FM::bytes(first * f.H),
                                      (shared ? f.sup : f.up) + FM::bytes(first * f.H)};
         const uint8_t* const sc[2] = {(shared ? f.sgate_s : f.gate_s) + first * (f.H / 32),
                                       (shared ? f.sup_s : f.up_s) + first * (f.H / 32)};
-        const int tok = n < rows ? (shared ? row0 + n : (int)tab.tok[row0 + n]) : 0;
-        auto load = [&](auto& b) { load_rows<FORM, NU>(f.x + (size_t)tok * f.H, n < rows, f.H, u0, cnt, b[0]); };
+        auto load = [&](auto& b) {
+#pragma unroll
+            for (int t = 0; t < (int)(sizeof(b) / sizeof(b[0])); ++t) {
+                const int r = t * kTile + n, tok = r < rows ? (shared ? row0 + r : (int)tab.tok[row0 + r]) : 0;
+                load_rows<FORM, NU>(f.x + (size_t)tok * f.H, r < rows, f.H, u0, cnt, b[t][0]);
+            }
+        };
         const int width = shared ? f.SF : f.F;
         uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + en) * width + ew;
-        run_steps<FORM, NU, 1>(w, sc, f.H, width, kTile, u0, cnt, s0, s1, ring, load, red, turn, [&](int s, float g, float u) {
+        auto done = [&](int s, float g, float u, int t) {
             // (an even thread stores its neighbour's column too)
             const float v = moe::silu(g) * u, v1 = moe::lanes::dpp<moe::lanes::kQuadXor1>(v);
             const uint32_t hi = moe::pack_bf16x2(v, v1);
             const uint32_t lo = moe::pack_bf16x2(v - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
-            if (en < rows && threadIdx.x % 2 == 0) {
-                *reinterpret_cast<uint32_t*>(h + s * kTile) = hi;
-                *reinterpret_cast<uint32_t*>(h + f.plane + s * kTile) = lo;
+            if (t * kTile + en < rows && threadIdx.x % 2 == 0) {
+                uint16_t* to = h + (size_t)(t * kTile) * width + s * kTile;
+                *reinterpret_cast<uint32_t*>(to) = hi;
+                *reinterpret_cast<uint32_t*>(to + f.plane) = lo;
             }
-        });
+        };
+        if (TB == 1 || rows <= kTile) run_steps<FORM, NU, 1, 1>(w, sc, f.H, width, kTile, u0, cnt, s0, s1, ring, load, red, turn, done);
+        else run_steps<FORM, NU, TB, 1>(w, sc, f.H, width, kTile, u0, cnt, s0, s1, ring, load, red, turn, done);
         at += s1 - s0;
     }
 }
 
 // -------------------------------------------------------------------- down --
-template <int FORM, int NU>
+template <int FORM, int NU, int TB>
 __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
 {
     using FM = Form<FORM>;
@@ -572,7 +604,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), n = lane & 15;
     const int en = threadIdx.x / 4 % 16, ew = threadIdx.x / 64 % 4 * 4 + threadIdx.x % 4;  // run_steps' done: row, column
-    const int entries = uni(tab.entries), sentries = f.SF ? (f.T + kTile - 1) / kTile : 0, each = f.H / (2 * kTile);
+    const int entries = uni(TB == 2 ? tab.live : tab.entries), sentries = f.SF ? (f.T + TB * kTile - 1) / (TB * kTile) : 0, each = f.H / (2 * kTile);
     const char* ring = rings + wave * kRingBytes;
     int at, end, turn = 0;
     my_run((int64_t)each * (entries * f.parts + sentries * f.sparts), at, end);
@@ -582,9 +614,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
         const bool shared = item >= entries * f.parts;
         if (shared) item -= entries * f.parts;
         const int parts = shared ? f.sparts : f.parts, entry = uni(item / parts), part = item - entry * parts;
-        const int e = shared ? 0 : uni((int)tab.entry_e[entry]);
-        const int row0 = shared ? entry * kTile : uni((int)tab.entry_row[entry]);
-        const int rows = shared ? min(kTile, f.T - row0) : uni((int)tab.entry_n[entry]);
+        const int e = shared ? 0 : uni((int)(TB == 2 ? tab.live_e : tab.entry_e)[entry]);
+        const int row0 = shared ? entry * TB * kTile : uni((int)(TB == 2 ? tab.live_row : tab.entry_row)[entry]);
+        const int rows = shared ? min(TB * kTile, f.T - row0) : uni((int)(TB == 2 ? tab.live_n : tab.entry_n)[entry]);
         const int K = shared ? f.SF : f.F, units = (K + FM::kUnit - 1) / FM::kUnit;
         const int p0 = uni(part * units / parts), pn = uni((part + 1) * units / parts) - p0;
         const int u0 = p0 + uni(wave * pn / kWaves), cnt = p0 + uni((wave + 1) * pn / kWaves) - u0;
@@ -593,19 +625,26 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
         const uint8_t* sbase = (shared ? f.sdown_s : f.down_s) + first * (K / 32);
         const uint8_t* const w[2] = {base, base + FM::bytes((size_t)kTile * K)};
         const uint8_t* const sc[2] = {sbase, sbase + kTile * (K / 32)};
-        const uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + (n < rows ? n : 0)) * K;
         auto load = [&](auto& b) {
-            load_rows<FORM, NU>(h, n < rows, K, u0, cnt, b[0]);
-            load_rows<FORM, NU>(h + f.plane, n < rows, K, u0, cnt, b[1]);
+#pragma unroll
+            for (int t = 0; t < (int)(sizeof(b) / sizeof(b[0])); ++t) {
+                const bool in = t * kTile + n < rows;
+                const uint16_t* h = (shared ? f.hs : f.h) + (size_t)(row0 + (in ? t * kTile + n : 0)) * K;
+                load_rows<FORM, NU>(h, in, K, u0, cnt, b[t][0]);
+                load_rows<FORM, NU>(h + f.plane, in, K, u0, cnt, b[t][1]);
+            }
         };
         float* y = (shared ? f.ys + (size_t)part * f.T * f.H : f.y + (size_t)part * f.N * f.H) +
                    (size_t)(row0 + en) * f.H + ew;
-        run_steps<FORM, NU, 2>(w, sc, K, f.H - kTile, 2 * kTile, u0, cnt, s0, s1, ring, load, red, turn, [&](int s, float a, float c) {
-            if (en < rows) {
-                y[s * 2 * kTile] = a;
-                y[s * 2 * kTile + kTile] = c;
+        auto done = [&](int s, float a, float c, int t) {
+            if (t * kTile + en < rows) {
+                float* to = y + (size_t)(t * kTile) * f.H + s * 2 * kTile;
+                to[0] = a;
+                to[kTile] = c;
             }
-        });
+        };
+        if (TB == 1 || rows <= kTile) run_steps<FORM, NU, 1, 2>(w, sc, K, f.H - kTile, 2 * kTile, u0, cnt, s0, s1, ring, load, red, turn, done);
+        else run_steps<FORM, NU, TB, 2>(w, sc, K, f.H - kTile, 2 * kTile, u0, cnt, s0, s1, ring, load, red, turn, done);
         at += s1 - s0;
     }
 }
@@ -653,54 +692,77 @@ hipError_t launch_logits(const moe_shape_t& s, const MoeFew& a, float* logits, h
     return hipGetLastError();
 }
 
-// Units of K that a wave takes at most, as the kernels' NU: 8192 values of H, 4096
-// of a part of F.
-template <int FORM>
-hipError_t launch_form(const Few& f, hipStream_t st)
+// Units of K that a wave takes at most, as the kernels' NU: 8192 values of H (4096 where
+// an entry has two tiles, whose rows take twice the registers), 4096 or 2048 of a part
+// of F. Of a wider x gate/up takes entries of 16 rows, and an expert with more reads
+// those weights twice.
+template <int FORM, int TB>
+hipError_t launch_gateup(const Few& f, int grid, hipStream_t st)
 {
-    const int unit = Form<FORM>::kUnit, grid = cu_count();
-    auto most = [&](int K, int parts) {
-        const int units = (K + unit - 1) / unit, part = parts ? (units + parts - 1) / parts : 0;
-        return (part + kWaves - 1) / kWaves;
-    };
-    const int gu = most(f.H, 1);
-    const int dn = most(f.F, f.parts) > most(f.SF, f.sparts) ? most(f.F, f.parts) : most(f.SF, f.sparts);
-#define MOE_FEW(N) few_gateup_kernel<FORM, N><<<grid, kThreads, 0, st>>>(f)
+    const int units = (f.H + Form<FORM>::kUnit - 1) / Form<FORM>::kUnit, n = (units + kWaves - 1) / kWaves;
+#define MOE_FEW(N) few_gateup_kernel<FORM, N, TB><<<grid, kThreads, 0, st>>>(f)
     if constexpr (FORM == MOE_W_BF16) {
-        if (gu <= 2) MOE_FEW(2);
-        else if (gu <= 4) MOE_FEW(4);
-        else if (gu <= 8) MOE_FEW(8);
-        else if (gu <= 14) MOE_FEW(14);
-        else MOE_FEW(16);
+        if (n <= 2) MOE_FEW(2);
+        else if (n <= 4) MOE_FEW(4);
+        else if (n <= 8) MOE_FEW(8);
+        if constexpr (TB == 1) {
+            if (n > 14) MOE_FEW(16);
+            else if (n > 8) MOE_FEW(14);
+        }
     } else if constexpr (FORM == MOE_W_MX8) {
-        if (gu <= 1) MOE_FEW(1);
-        else if (gu <= 2) MOE_FEW(2);
-        else if (gu <= 4) MOE_FEW(4);
-        else if (gu <= 7) MOE_FEW(7);
-        else MOE_FEW(8);
+        if (n <= 1) MOE_FEW(1);
+        else if (n <= 2) MOE_FEW(2);
+        else if (n <= 4) MOE_FEW(4);
+        if constexpr (TB == 1) {
+            if (n > 7) MOE_FEW(8);
+            else if (n > 4) MOE_FEW(7);
+        }
     } else {
-        if (gu <= 1) MOE_FEW(1);
-        else if (gu <= 2) MOE_FEW(2);
-        else MOE_FEW(4);
-    }
-#undef MOE_FEW
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-#define MOE_FEW(N) few_down_kernel<FORM, N><<<grid, kThreads, 0, st>>>(f)
-    if constexpr (FORM == MOE_W_BF16) {
-        if (dn <= 2) MOE_FEW(2);
-        else if (dn <= 4) MOE_FEW(4);
-        else MOE_FEW(8);
-    } else if constexpr (FORM == MOE_W_MX8) {
-        if (dn <= 1) MOE_FEW(1);
-        else if (dn <= 2) MOE_FEW(2);
-        else MOE_FEW(4);
-    } else {
-        if (dn <= 1) MOE_FEW(1);
-        else MOE_FEW(2);
+        if (n <= 1) MOE_FEW(1);
+        else if (n <= 2) MOE_FEW(2);
+        if constexpr (TB == 1)
+            if (n > 2) MOE_FEW(4);
     }
 #undef MOE_FEW
     return hipGetLastError();
+}
+
+template <int FORM, int TB>
+hipError_t launch_down(const Few& f, int grid, hipStream_t st)
+{
+    auto most = [&](int K, int parts) {
+        const int units = (K + Form<FORM>::kUnit - 1) / Form<FORM>::kUnit, part = parts ? (units + parts - 1) / parts : 0;
+        return (part + kWaves - 1) / kWaves;
+    };
+    const int n = most(f.F, f.parts) > most(f.SF, f.sparts) ? most(f.F, f.parts) : most(f.SF, f.sparts);
+#define MOE_FEW(N) few_down_kernel<FORM, N, TB><<<grid, kThreads, 0, st>>>(f)
+    constexpr int kMost = moe::kFewPart / TB / Form<FORM>::kUnit / kWaves;  // 8, 4, 2 or, of two tiles, 4, 2, 1
+    if constexpr (kMost >= 8) {
+        if (n <= 2) MOE_FEW(2);
+        else if (n <= 4) MOE_FEW(4);
+        else MOE_FEW(8);
+    } else if constexpr (kMost >= 4) {
+        if (n <= kMost / 4) MOE_FEW(kMost / 4);
+        else if (n <= kMost / 2) MOE_FEW(kMost / 2);
+        else MOE_FEW(kMost);
+    } else if constexpr (kMost == 2) {
+        if (n <= 1) MOE_FEW(1);
+        else MOE_FEW(2);
+    } else {
+        MOE_FEW(1);
+    }
+#undef MOE_FEW
+    return hipGetLastError();
+}
+
+template <int FORM>
+hipError_t launch_form(const Few& f, hipStream_t st)
+{
+    const int grid = cu_count();
+    const bool two = f.two_tiles;
+    const hipError_t e = two && f.H <= moe::kFewMaxH / 2 ? launch_gateup<FORM, 2>(f, grid, st) : launch_gateup<FORM, 1>(f, grid, st);
+    if (e != hipSuccess) return e;
+    return two ? launch_down<FORM, 2>(f, grid, st) : launch_down<FORM, 1>(f, grid, st);
 }
 
 }  // namespace
@@ -713,7 +775,8 @@ hipError_t moe_launch_few(const moe_shape_t& s, const MoeFew& a, char* ws, hipSt
     Few f;
     f.T = s.T, f.H = s.H, f.E = s.E, f.k = s.k, f.F = s.F, f.SF = a.shared_F, f.N = s.T * s.k;
     f.planes = moe::few_logit_parts(s.H);
-    f.parts = moe::few_parts(s.F), f.sparts = moe::few_parts(a.shared_F);
+    f.two_tiles = moe::few_two_tiles(s);
+    f.parts = moe::few_parts(s.F, f.two_tiles), f.sparts = moe::few_parts(a.shared_F, f.two_tiles);
     f.x = static_cast<const uint16_t*>(a.x);
     float* logits = reinterpret_cast<float*>(ws + L.logits);
     f.logits = logits, f.bias = a.bias;

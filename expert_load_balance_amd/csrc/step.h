@@ -128,6 +128,7 @@ namespace moe {
 
 constexpr int kFewMaxH = 8192;   // a wave's part of a row of x stays in registers
 constexpr int kFewPart = 4096;   // values of K of a part of the down projection (h in registers, two bf16 each)
+constexpr int kFewTile = 16;     // rows of a tile
 
 constexpr int kFewTableBytes = 8192; // rows and entries of the choice, at most
 constexpr int kFewLogitK = 1024; // values of H of a part of the router's scores
@@ -135,7 +136,17 @@ constexpr int kFewLogitParts = kFewMaxH / kFewLogitK;
 
 inline int few_logit_parts(int H) { return (H + kFewLogitK - 1) / kFewLogitK; }
 inline int few_unit(int form) { return form == MOE_W_BF16 ? 64 : 128; }
-inline int few_parts(int F) { return (F + kFewPart - 1) / kFewPart; }
+// Whether an expert's rows may be two tiles, so that its weights are read once: where
+// experts have more than 8 rows on average. (Two tiles' h takes parts of half the
+// length. us, one tile and two: 4 experts, all chosen by 17 tokens, 4096 x 14336, 8-bit 248
+// and 161; 4-bit, top-8 of 16, 4096 x 4096, 17 tokens (8.5 rows) 99.5 and 100.7, 24
+// tokens 125 and 105 to 117; 4-bit, top-2 of 8, 4096 x 14336, 32 tokens (8 rows) 151 and 162.)
+inline bool few_two_tiles(const moe_shape_t& s) { return s.T > kFewTile && s.T * s.k > 8 * s.E; }
+inline int few_parts(int F, bool two_tiles)
+{
+    const int part = two_tiles ? kFewPart / 2 : kFewPart;
+    return (F + part - 1) / part;
+}
 
 // logits [parts][T][E], the router's w [N], each assignment's row [N], the choice's tables, h in two bf16
 // planes [N][F] + [T][shared_F], y fp32 [parts][N][H] + [shared parts][T][H]
@@ -156,8 +167,8 @@ inline FewWsLayout few_ws_layout(const moe_shape_t& s, int shared_F)
     w.h_shared = N * s.F;
     w.h_plane = w.h_shared + (size_t)s.T * shared_F;
     w.h = o;      o = align256(o + 2 * w.h_plane * 2);
-    w.y_shared = (size_t)few_parts(s.F) * N * s.H;
-    w.y = o;      o = align256(o + (w.y_shared + (size_t)few_parts(shared_F) * s.T * s.H) * 4);
+    w.y_shared = (size_t)few_parts(s.F, few_two_tiles(s)) * N * s.H;
+    w.y = o;      o = align256(o + (w.y_shared + (size_t)few_parts(shared_F, few_two_tiles(s)) * s.T * s.H) * 4);
     w.total = o;
     return w;
 }

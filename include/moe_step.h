@@ -148,8 +148,10 @@ size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t s
  *            (+ the same of the shared expert, weight 1), rounded once to bf16.
  * Products are of bf16 values (blocks widen to bf16 exactly) with fp32 sums; h
  * keeps 16 bits of its value (two bf16), so that bf16's rounding of out is the
- * only one that counts. Each live expert's weights are read once for all of its
- * tokens. No plan, no dispatch: R and S of the shape are not used.
+ * only one that counts. Each live expert's weights are read once for up to 16
+ * of its tokens, and once for all of them where experts have more than 8 on
+ * average (gate and up: if H <= 4096). No plan, no dispatch: R and S of the
+ * shape are not used.
  *   shape: dtype MOE_BF16; form a moe_weight_form_t, for the routed and the
  *   shared experts; MOE_W_MX8 and MOE_W_MX4 need H, F and shared_F multiples
  *   of 128, MOE_W_BF16 of 64; H <= 8192; H * F and H * shared_F below 2^31 - 64;

@@ -227,3 +227,38 @@ def test_a_bad_weight_reaches_its_rows_only(form):
             assert torch.equal(L.out[on][:, keep], ref_out[on][:, keep])
         else:
             assert bool(torch.isnan(L.out[on]).all())
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+@pytest.mark.parametrize("T,H,E,k,F,SF", [(17, 512, 4, 4, 256, 128), (32, 4096, 6, 3, 384, 256), (24, 4224, 5, 4, 256, 256),
+                                          (29, 256, 40, 8, 2176, 0), (32, 1024, 2, 1, 128, 4224), (20, 2048, 8, 7, 4352, 0)])
+def test_experts_with_one_and_two_tiles_of_rows(T, H, E, k, F, SF, form):
+    """More than 16 tokens: experts with more than 16 rows beside ones with fewer, the
+    bits of a call repeated, and nothing kept from what the workspace held."""
+    case = (T, H, E, k, F, SF, form)
+    print("[case]", case, flush=True)
+    L, x, wr, bias, w, shared = layer(case, 3)
+    bias[0] += 1.5                                       # (an expert that most tokens choose)
+    outs = []
+    for fill in (0xFF, 0x7F, 0):
+        L.ws.fill_(fill)
+        L.forward(x, wr, bias, *w, shared)
+        torch.cuda.synchronize()
+        outs.append(L.out.clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    check(L, x, wr, bias, w, shared, str(case))
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+@pytest.mark.parametrize("T,H,E,k,F,SF", [(32, 512, 16, 2, 256, 4224), (27, 256, 40, 8, 4352, 128), (32, 4352, 8, 2, 128, 0)])
+def test_a_full_expert_among_sparse_ones(T, H, E, k, F, SF, form):
+    """Entries of 16 rows: an expert that every token chooses has two."""
+    case = (T, H, E, k, F, SF, form)
+    print("[case]", case, flush=True)
+    L, x, wr, bias, w, shared = layer(case, 4)
+    bias[E // 2] += 30
+    L.ws.fill_(0xFF)
+    L.forward(x, wr, bias, *w, shared)
+    torch.cuda.synchronize()
+    assert bool((L.ids == E // 2).any(-1).all())
+    check(L, x, wr, bias, w, shared, str(case))
