@@ -33,6 +33,7 @@
 
 #include "lanes.h"
 #include "lds_pipe.h"
+#include "split.h"
 #include "step.h"
 
 namespace {
@@ -618,7 +619,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(const Few f)
         const int row0 = shared ? entry * TB * kTile : uni((int)(TB == 2 ? tab.live_row : tab.entry_row)[entry]);
         const int rows = shared ? min(TB * kTile, f.T - row0) : uni((int)(TB == 2 ? tab.live_n : tab.entry_n)[entry]);
         const int K = shared ? f.SF : f.F, units = (K + FM::kUnit - 1) / FM::kUnit;
-        const int p0 = uni(part * units / parts), pn = uni((part + 1) * units / parts) - p0;
+        const int p0 = uni(moe::part_begin(part, units, parts)), pn = uni(moe::part_begin(part + 1, units, parts)) - p0;
         const int u0 = p0 + uni(wave * pn / kWaves), cnt = p0 + uni((wave + 1) * pn / kWaves) - u0;
         const size_t first = (size_t)e * f.H;
         const uint8_t* base = (shared ? f.sdown : f.down) + FM::bytes(first * K);
