@@ -537,6 +537,19 @@ __device__ __forceinline__ void my_run(int64_t total, int& a, int& z)
 }
 
 // ---------------------------------------------------------------- gate, up --
+// a and b as two bf16 each: their rounding, a pair a word, and what it leaves of them (lo).
+// A value that would round to an infinity is cut, so that what is left is finite; an
+// infinite one leaves nothing. (As a difference either would be infinite or NaN, and out NaN.)
+__device__ __forceinline__ uint32_t two_bf16(float a, float b, uint32_t& lo)
+{
+    uint32_t hi = moe::pack_bf16x2(a, b);
+    if ((hi & 0x7fffu) == 0x7f80u) hi = (hi & 0xffff0000u) | __float_as_uint(a) >> 16;
+    if ((hi & 0x7fff0000u) == 0x7f800000u) hi = (hi & 0xffffu) | (__float_as_uint(b) & 0xffff0000u);
+    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+    lo = moe::pack_bf16x2(isinf(a) ? 0.0f : ra, isinf(b) ? 0.0f : rb);
+    return hi;
+}
+
 // TB: tiles of 16 rows that an entry has at most.
 template <int FORM, int NU, int TB>
 __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
@@ -579,8 +592,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_gateup_kernel(const Few f)
         auto done = [&](int s, float g, float u, int t) {
             // (an even thread stores its neighbour's column too)
             const float v = moe::silu(g) * u, v1 = moe::lanes::dpp<moe::lanes::kQuadXor1>(v);
-            const uint32_t hi = moe::pack_bf16x2(v, v1);
-            const uint32_t lo = moe::pack_bf16x2(v - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
+            uint32_t lo;
+            const uint32_t hi = two_bf16(v, v1, lo);
             if (t * kTile + en < rows && threadIdx.x % 2 == 0) {
                 uint16_t* to = h + (size_t)(t * kTile) * width + s * kTile;
                 *reinterpret_cast<uint32_t*>(to) = hi;

@@ -1,11 +1,13 @@
-"""moe_few_layer at the ends of its ranges: the widest shared expert."""
+"""moe_few_layer at the ends of its ranges: the widest shared expert, values of h next to
+and past the largest bf16."""
 import pytest
 
 torch = pytest.importorskip("torch")
 import expert_load_balance_amd as moe  # noqa: E402
 from expert_load_balance_amd.layer import MoeLayerFew  # noqa: E402
 
-from test_gpu_few import BF, DEV, check, gen, randn  # noqa: E402
+import step_ref as ref  # noqa: E402
+from test_gpu_few import BF, DEV, blocks, check, gen, randn  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,32 @@ def test_the_widest_shared_expert(T):
     L.forward(x, wr, bias, *w, [(gate, None), (up, None), (down, None)])
     torch.cuda.synchronize()
     check(L, x, wr, bias, w, [(gate[:, at], None), (up[:, at], None), (few_down, None)], f"T {T}")
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx8", "mx4"])
+@pytest.mark.parametrize("column", [5, 66])
+def test_h_next_to_and_past_the_largest_value(form, column):
+    """One column of h is 1.996 * 2^127, which float32 holds and bf16's rounding makes
+    infinite, or twice that, which is infinite in float32; the others are 0. Every product
+    and sum is exact but for silu's quotient (2^-22 of it at most) and out's rounding."""
+    T, H, F = 5, 128, 128
+    x = torch.zeros(T, H)
+    x[:, 0] = torch.tensor([1.0, 1.0, -1.0, 1.0, -1.0])
+    x[:, 1] = torch.tensor([1.328125, 1.328125, -1.328125, -1.328125, -1.328125])   # u 2^121 times 1.996 or 2^-8
+    x[:, 32] = torch.tensor([1.0, 2.0, 1.0, 1.0, 2.0])                               # g 64 or 128
+    gate, up, down = torch.zeros(1, F, H), torch.zeros(1, F, H), torch.zeros(1, H, F)
+    gate[0, column, 32] = 64.0
+    up[0, column, 0], up[0, column, 1] = 2.0 ** 121, 0.75 * 2.0 ** 121
+    down[0, :, column] = 2.0 ** -100
+    down[0, ::3, column] = -2.0 ** -101
+    w = [blocks(form, v.to(DEV)) for v in (gate, up, down)]
+    L = MoeLayerFew(moe.Shape(T, H, 1, 1, F, 1, 0, moe.MOE_BF16), DEV, weights=form)
+    L.forward(x.to(DEV).to(BF), torch.zeros(1, H, dtype=BF, device=DEV), None, *w)
+    torch.cuda.synchronize()
+    h = x[:, 32].double() * 64 * (x[:, 0].double() + 0.75 * x[:, 1].double()) * 2.0 ** 121
+    want = (h[:, None] * down[0, :, column].double()).to(DEV)
+    fits = torch.tensor([0, 2, 3], device=DEV)
+    assert h[0] == 1.99609375 * 2.0 ** 127 and float(h[:1].to(BF)) == float("inf")
+    ref.check(L.out[fits], (want[fits], want[fits].abs() * 2.0 ** -22), "out", BF)
+    for t in (1, 4):
+        assert torch.equal(L.out[t].float(), torch.sign(want[t]).float() * float("inf")), t
