@@ -146,12 +146,14 @@ size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t s
  *   out[t] = sum_j w[t][j] * W_down[e] (silu(W_gate[e] x_t) * (W_up[e] x_t)),
  *            e = ids[t][j], in j order of sums in fp32
  *            (+ the same of the shared expert, weight 1), rounded once to bf16.
- * Products are of bf16 values (blocks widen to bf16 exactly) with fp32 sums; h
- * keeps 16 bits of its value (two bf16), so that bf16's rounding of out is the
- * only one that counts. Each live expert's weights are read once for up to 16
- * of its tokens, and once for all of them where experts have more than 8 on
- * average (gate and up: if H <= 4096). No plan, no dispatch: R and S of the
- * shape are not used.
+ * Products are of bf16 values with fp32 sums; h keeps 16 bits of its value (two
+ * bf16), so that bf16's rounding of out is the only one that counts. Blocks widen
+ * to bf16: exactly, with scales of 2^-124 to 2^119 (8-bit codes) and up to 2^125
+ * (4-bit codes); beyond, values that bf16 does not hold round to it or are infinite.
+ * Products and sums below 2^-126 may be taken as zero. Each live expert's weights
+ * are read once for up to 16 of its tokens, and once for all of them where experts
+ * have more than 8 on average (gate and up: if H <= 4096). No plan, no dispatch: R
+ * and S of the shape are not used.
  *   shape: dtype MOE_BF16; form a moe_weight_form_t, for the routed and the
  *   shared experts; MOE_W_MX8 and MOE_W_MX4 need H, F and shared_F multiples
  *   of 128, MOE_W_BF16 of 64; H <= 8192; H * F and H * shared_F below 2^31 - 64;

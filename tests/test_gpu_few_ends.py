@@ -64,3 +64,35 @@ def test_h_next_to_and_past_the_largest_value(form, column):
     ref.check(L.out[fits], (want[fits], want[fits].abs() * 2.0 ** -22), "out", BF)
     for t in (1, 4):
         assert torch.equal(L.out[t].float(), torch.sign(want[t]).float() * float("inf")), t
+
+
+@pytest.mark.parametrize("form,lowest,highest", [("mx8", 3, 246), ("mx4", 0, 252)])
+def test_scales_at_the_ends_of_their_range(form, lowest, highest):
+    """W_down with a scale byte of its own in every row (2^-124 to 2^119 for 8-bit codes, 2^-127
+    to 2^125 for 4-bit ones widen to bf16 exactly), times an h of about 2^108, 2^8 and 2^-92: the
+    products that float32 holds come out as the layer's do in general (bounds as in step_ref's
+    swiglu, h exact)."""
+    T, H, F = 3, 256, 256
+    g = gen(1)
+    x = torch.zeros(T, H)
+    x[:, 0], x[:, 32] = 1, torch.tensor([2.0 ** 100, 1.0, 2.0 ** -100])
+    gate, up = (torch.zeros(1, F, H, device=DEV) for _ in range(2))
+    gate[0, :, 0] = 64
+    up[0, :, 32] = torch.randint(1, 7, (F,), generator=g, device=DEV) * torch.sign(randn(g, F))
+    q = torch.randint(0, 256, (1, H, F if form == "mx8" else F // 2), generator=g, device=DEV)
+    if form == "mx8":
+        q = torch.where(q % 128 == 127, q - 1, q)          # (the codes that are NaN)
+    s = torch.arange(H, device=DEV).clamp(max=254).to(torch.uint8)[None, :, None].expand(1, H, F // 32).contiguous()
+    w = [blocks(form, gate), blocks(form, up), (q.to(torch.uint8), s)]
+    L = MoeLayerFew(moe.Shape(T, H, 1, 1, F, 1, 0, moe.MOE_BF16), DEV, weights=form)
+    x = x.to(DEV).to(BF)
+    L.forward(x, torch.zeros(1, H, dtype=BF, device=DEV), None, *w)
+    torch.cuda.synchronize()
+    G, U, D = (ref.whole(m, 0) for m in w)
+    h = (x.double() @ G.t()) * (x.double() @ U.t())         # silu(64) is 64 but for 2^-90 of it
+    want, size = h @ D.t(), h.abs() @ D.abs().t()
+    byte = torch.arange(H, device=DEV)
+    inside = (byte >= lowest) & (byte <= highest) & (size < 2.0 ** 126) & (size > 2.0 ** -100)
+    assert bool(inside.any(0)[lowest:highest + 1].all())
+    tol = (F / 128 + 24) * 2.0 ** -22 * size
+    ref.check(L.out[inside], (want[inside], tol[inside]), form, BF)
