@@ -537,9 +537,10 @@ __device__ __forceinline__ Unit unit_of(const Gemm& g, const KindWork& w, int j)
     }
     // If every workgroup walked K from the same stage, the lines in flight would
     // share their low address bits where rows are a multiple of 4 KB apart, and
-    // crowd a few memory channels. So the XCDs start four stages apart (a whole
-    // group of scales; K a multiple of 512 values, so that no group is cut
-    // short); within one, tiles stay in step for what they share in its L2.
+    // crowd a few memory channels. So the XCDs start four stages apart (of 128
+    // values a whole group of scales, and only where K has no group cut short; of
+    // 256 values two groups, and the last stage may be half a one: see cut); within
+    // one, tiles stay in step for what they share in its L2.
     // Measured, no stagger / by N-tile / by XCD: gate/up of 128 x 16 rows of
     // 4096 x 1536 388 / 339 / 326 us; down of 256 x 256 rows of 7168 x 2048
     // 1209 / (by N-tile on 4 KB rows only) / 1158 us; 8 x 512 rows of 4096 x 14336
