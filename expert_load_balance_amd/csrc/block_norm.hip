@@ -567,14 +567,28 @@ hipError_t launch_fwd(const Fwd& a, int rows, hipStream_t st)
     return hipGetLastError();
 }
 
+// One vector a thread; two of fp32, whose kernel spills 28 vector registers; two of bf16
+// spill 182, and the wide kernel takes those rows. One gate a channel, us, two vectors
+// and wide: bf16 8192 x 8256 844 and 626, 8192 x 16384 1215 and 1177, 1024 x 12288 168 and
+// 124; fp32 8192 x 4160 172 and 487, 8192 x 8192 301 and 928, 1024 x 7168 60 and 111.
 template <bool BF16, bool STREAM>
 hipError_t launch_bwd(const Bwd& a, hipStream_t st)
 {
     const int G = a.p.grid, t = (a.vecs + 63) / 64 * 64;
-    if (t <= 512) block_norm_bwd_kernel<BF16, 1, 512, STREAM><<<G, t, 0, st>>>(a);
-    else if (t <= 1024) block_norm_bwd_kernel<BF16, 1, 1024, STREAM><<<G, t, 0, st>>>(a);
-    else if (t <= 2048) block_norm_bwd_kernel<BF16, 2, 1024, STREAM><<<G, (a.vecs + 127) / 128 * 64, 0, st>>>(a);
-    else block_norm_bwd_wide_kernel<BF16><<<G, kMaxThreads, 0, st>>>(a);
+    if (t <= 512) {
+        block_norm_bwd_kernel<BF16, 1, 512, STREAM><<<G, t, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    if (t <= 1024) {
+        block_norm_bwd_kernel<BF16, 1, 1024, STREAM><<<G, t, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    if constexpr (!BF16)
+        if (t <= 2048) {
+            block_norm_bwd_kernel<BF16, 2, 1024, STREAM><<<G, (a.vecs + 127) / 128 * 64, 0, st>>>(a);
+            return hipGetLastError();
+        }
+    block_norm_bwd_wide_kernel<BF16><<<G, kMaxThreads, 0, st>>>(a);
     return hipGetLastError();
 }
 
