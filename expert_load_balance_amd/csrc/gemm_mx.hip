@@ -665,8 +665,11 @@ struct Copier {
         if constexpr (GE::kPanels == 2) {
             k0 = u.k0;
             half = K % (2 * kTK) ? stages<KIND, WB>(K) - 1 - u.k0 : -1;
-            // (a group of 16 bytes may reach past a row's end, and the last row's past the array)
-            arange = uni((int)((uint32_t)(g.N - (int)x0) * (uint32_t)KS));
+            // (a group of 16 bytes may reach past a row's end, and the last row's past the
+            // array; of h no more than a tile's rows and the next one, so that the range stays
+            // within 32 bits, whatever N * KS is: N * H is below 2^31, N * F below 2^40)
+            const int rows = MODE == kGateUp ? g.N : min(g.N - (int)x0, GE::kRows + 1);
+            arange = uni((int)((uint32_t)rows * (uint32_t)KS));
             wrange = uni((int)((uint32_t)wrows * (uint32_t)KS));
         }
         st = scalar<0>();
