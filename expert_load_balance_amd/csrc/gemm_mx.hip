@@ -56,10 +56,13 @@
 // The first is bound by what a stage of a small tile does in turn (copies out, reads,
 // splitting the rows' codes, products) on one wave a SIMD.
 //
-// Registers: the 256-row kernels fill the vector registers (243 and 251 and 256
-// accumulators) and spill 128 (gate/up) and 116 (down) scalars to lanes of vector
-// registers, held across a tile's stages for the code between tiles; the stages'
-// own addresses are not among them. The down kernels keep 20 bytes a lane in scratch.
+// Registers: the 256-row kernels fill the vector registers (244 in gate/up and 252 in
+// down, and 256 accumulators; 216 on 4-bit weights) and spill scalars to lanes of vector
+// registers, held across a tile's stages for the code between tiles. On 8-bit weights
+// these are 128 (gate/up) and 115 (down), the stages' own addresses not among them; on
+// 4-bit weights 362 and 195, of which a stage of the small tiles reads up to 19 back (gate/up
+// of 32 rows). The 8-bit down kernels keep 20 bytes a lane in scratch, the 4-bit one without
+// 256-row tiles 36.
 #include <type_traits>
 #include <utility>
 
@@ -1503,7 +1506,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mx_kernel(const Gemm g)
 
 // Whether a launch may cut tiles along K: not where the rows alone make
 // kSplitRounds rounds of tiles, whatever their experts (the fixup then need not
-// be launched, 5 us), nor where K has no two parts.
+// be launched, 5 us), nor where K has no two parts. (Counted in stages of 128 values: small
+// tiles of 4-bit weights, of stages of 256, are not cut below K = 1920, and where K is 1024
+// and more the fixup is launched for them all the same, and finds nothing.)
 inline bool may_split(const moe_shape_t& s, int mode, int P)
 {
     const int64_t N = (int64_t)s.T * s.k, ntn = mode == kGateUp ? s.F / (kTN / 2) : (s.H + kTN - 1) / kTN;

@@ -240,7 +240,9 @@ class MoeLayerFew:
     A bf16 shape; weights: "bf16", "mx8" or "mx4", the form of every projection;
     shared_F: width of an always-on shared expert of the same form (None: no shared
     expert). The buffers belong to one call at a time: calls that may overlap, and
-    captured graphs that may, take an object each.
+    captured graphs that may, take an object each. On 4-bit weights MoeLayerMx can be
+    faster where more than 16 tokens choose and an expert has more than 12 of them on
+    average (by a fifth at 32 tokens that choose every expert).
     """
 
     FORMS = {"bf16": MOE_W_BF16, "mx8": MOE_W_MX8, "mx4": MOE_W_MX4}

@@ -67,7 +67,9 @@ size_t moe_block_norm_backward_workspace_bytes(const moe_shape_t *shape, int32_t
  *   dx = rstd_post * (dn * w_post - xhat * mean(dn * w_post * xhat));
  *   dw_pre = sum over rows of dy * shat, dw_post of dn * xhat.
  * fp32 throughout, dx and dresidual rounded once; sums over rows are added in
- * an order fixed by the shape and gate_rows.
+ * an order fixed by the shape and gate_rows. dx's mean and a token's dgate are
+ * differences of two sums, of what ds and dy give and of what the other mean takes
+ * away: they are good to fp32's roundings of those sums' terms, not of d's.
  *   d_x, alpha, d_w_post, d_gate, gate_rows, d_w_pre as the forward's; d_s
  *   dtype[T][H], d_rstd_post, d_rstd_pre float[T] the forward's outputs;
  *   d_dy dtype[T][H] (the gradient of y) or NULL (none: d_w_pre, d_s,
@@ -97,8 +99,9 @@ moe_status_t moe_mx4_quantize(int64_t rows, int64_t cols, int32_t dtype, const v
                               void *d_q, void *d_scales, moe_stream_t stream);
 
 /* The values of 4-bit blocks, code * 2^e rounded to dtype (bf16 holds every
- * value of magnitude 2^-126 and more exactly; below, bf16's subnormals round). A
- * scale byte of 255 gives NaN.
+ * value of magnitude 2^-126 and more exactly; below, bf16's subnormals round; 2^128
+ * and more, the largest codes of scales of 2^126 and 2^127, are infinite). A scale
+ * byte of 255 gives NaN.
  *   d_q uint8[rows][cols/2], d_scales uint8[rows][cols/32]; d_x
  *   dtype[rows][cols] out; limits as moe_mx4_quantize. */
 moe_status_t moe_mx4_dequantize(int64_t rows, int64_t cols, int32_t dtype, const void *d_q,
@@ -111,7 +114,10 @@ size_t moe_mx4_workspace_bytes(const moe_shape_t *shape);
 
 /* moe_grouped_gemm_mx with weights in 4-bit blocks: rows and h stay in 8-bit
  * blocks, the products are the scaled matrix instructions' of 4-bit by 8-bit
- * codes, with their precision as described there.
+ * codes, with their precision as described there; but gate and up of experts of up
+ * to 64 rows are multiplied in two parts of the rows' codes, which the cut leaves
+ * whole but for their last bits, where 8-bit weights take bf16 products. y is
+ * rounded to bf16 before the combine, as there.
  *   d_a, d_a_scales uint8[N][H], uint8[N][H/32] (moe_permute_mx's buffer);
  *   d_w_gate, d_w_up uint8[E][F][H/2] with scales uint8[E][F][H/32];
  *   d_w_down uint8[E][H][F/2] with scales uint8[E][H][F/32]; d_plan from
@@ -153,7 +159,11 @@ size_t moe_few_workspace_bytes(const moe_shape_t *shape, int32_t form, int32_t s
  * Products and sums below 2^-126 may be taken as zero. Each live expert's weights
  * are read once for up to 16 of its tokens, and once for all of them where experts
  * have more than 8 on average (gate and up: if H <= 4096). No plan, no dispatch: R
- * and S of the shape are not used.
+ * and S of the shape are not used. The calls on 8-bit rows (moe_permute_mx and
+ * moe_grouped_gemm_mx or _mx4) are about as fast on 8-bit weights where more than 16
+ * tokens choose, and an expert has more than 12 of them on average (T * k / E); on
+ * 4-bit weights they then take from a tenth more to a fifth less (32 tokens, every
+ * expert chosen by all). With fewer they are slower.
  *   shape: dtype MOE_BF16; form a moe_weight_form_t, for the routed and the
  *   shared experts; MOE_W_MX8 and MOE_W_MX4 need H, F and shared_F multiples
  *   of 128, MOE_W_BF16 of 64; H <= 8192; H * F and H * shared_F below 2^31 - 64;
